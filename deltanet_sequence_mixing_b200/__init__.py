@@ -8,6 +8,11 @@ library's CUDA kernels.  There is no CPU fallback.
     o, S = deltanet_chunk_fwd(q, k, v, beta, alpha=None, S0=None, C=64, prestep=False)
     o    = deltanet_decode_step(q, k, v, beta, S, alpha=None, prestep=False)  # S in place
     o, S, z = linear_attn_fwd(q, k, v, S0=None, z0=None, C=64)
+    o, S = gated_linear_attn_fwd(q, k, v, alpha=None, S0=None)
+    g    = gated_linear_attn_bwd(q, k, v, dO, alpha=None, S0=None, dS_T=None)
+    o    = gated_linear_attn_decode_step(q, k, v, S, alpha=None)  # S in place
+    q, k = qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, inv_freq)
+    g    = qk_norm_rope_bwd(q, k, dq, dk, q_weight, k_weight, positions, inv_freq)
 """
 from __future__ import annotations
 
@@ -21,6 +26,8 @@ from ._lib import DeltaNetError, check, lib, status_string  # noqa: F401
 __all__ = [
     "deltanet_chunk_fwd", "deltanet_chunk_fwd_host", "deltanet_decode_step", "linear_attn_fwd",
     "deltanet_chunk_bwd", "seq_segments",
+    "gated_linear_attn_fwd", "gated_linear_attn_bwd", "gated_linear_attn_decode_step",
+    "qk_norm_rope_fwd", "qk_norm_rope_bwd",
     "workspace_for", "host_workspace_for",
     "deltanet_get_device_status", "deltanet_selftest_wait_timeout", "DeltaNetError",
 ]
@@ -278,6 +285,247 @@ def deltanet_decode_step(q, k, v, beta, S, alpha=None, o=None, prestep: bool = F
             _ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(alpha), _ptr(S), _ptr(o),
             B, H, Dk, Dv, _DT[dtype], opts, _stream(dev)))
     return o
+
+
+def _need_shape(t, name, shape, dtype, device):
+    """A contiguous tensor of this shape, type and device (None passes)."""
+    if t is not None:
+        _need(t, name, dtype, device)
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _own_workspace(device, nbytes: int) -> torch.Tensor:
+    """The workspace of one call: the status word alone is shared (kernels only
+    ever set bits in it); scratch comes from the caching allocator for each
+    call, so calls on several streams and captured graphs never share it."""
+    if nbytes <= 256 and not torch.cuda.is_current_stream_capturing():
+        return workspace_for(device)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    check("deltanet_workspace_init",
+          lib().deltanet_workspace_init(_ptr(ws), ws.numel(), _stream(device)))
+    return ws
+
+
+def _recurrence_inputs(q, k, v, alpha, rank):
+    """Sizes of a gated recurrence call, its inputs checked."""
+    _need(q, "q")
+    dev, dtype = q.device, q.dtype
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype}")
+    if q.dim() != rank:
+        raise ValueError(f"q must have {rank} dimensions, got {q.dim()}")
+    lead, Dk = q.shape[:-1], q.shape[-1]
+    _need(v, "v", dtype, dev)
+    if v.dim() != rank:
+        raise ValueError(f"v must have {rank} dimensions, got {v.dim()}")
+    Dv = v.shape[-1]
+    _need_shape(k, "k", q.shape, dtype, dev)
+    if k is None:
+        raise TypeError("k must be a torch.Tensor")
+    _need_shape(v, "v", (*lead, Dv), dtype, dev)
+    _need_shape(alpha, "alpha", lead, torch.float32, dev)
+    return dev, dtype, lead, Dk, Dv
+
+
+def _gated_bytes(fn, B, H, T, Dk, Dv, dtype):
+    n = getattr(lib(), fn)(B, H, T, Dk, Dv, _DT[dtype])
+    if n == 0:
+        raise DeltaNetError(fn, _lib.DN_ERR_UNSUPPORTED)
+    return n
+
+
+def gated_linear_attn_fwd(q, k, v, alpha=None, S0=None, o=None, S_out=None, workspace=None):
+    """Gated linear recurrence S_t = alpha_t S_{t-1} + k_t^T v_t, o_t = q_t S_t.
+    q, k: (B,H,T,Dk); v: (B,H,T,Dv) (bf16 or f32); alpha: (B,H,T) f32 in [0,1]
+    or None (1); S0: (B,H,Dk,Dv) f32 or None (0).  S_out may be S0.  Returns
+    (o, S_out): (B,H,T,Dv) of q's type and (B,H,Dk,Dv) f32."""
+    dev, dtype, (B, H, T), Dk, Dv = _recurrence_inputs(q, k, v, alpha, 4)
+    _need_shape(S0, "S0", (B, H, Dk, Dv), torch.float32, dev)
+    with torch.cuda.device(dev):
+        if o is None:
+            o = torch.empty(B, H, T, Dv, dtype=dtype, device=dev)
+        if S_out is None:
+            S_out = torch.empty(B, H, Dk, Dv, dtype=torch.float32, device=dev)
+        _need_shape(o, "o", (B, H, T, Dv), dtype, dev)
+        _need_shape(S_out, "S_out", (B, H, Dk, Dv), torch.float32, dev)
+        ws = workspace
+        if ws is None:
+            ws = _own_workspace(dev, _gated_bytes("gated_linear_attn_workspace_bytes", B, H, T, Dk, Dv, dtype))
+        _need(ws, "workspace", torch.uint8, dev)
+        check("gated_linear_attn_fwd", lib().gated_linear_attn_fwd(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(S0), _ptr(o), _ptr(S_out),
+            B, H, T, Dk, Dv, _DT[dtype], _ptr(ws), ws.numel(), _stream(dev)))
+    return o, S_out
+
+
+def gated_linear_attn_bwd(q, k, v, dO, alpha=None, S0=None, dS_T=None, workspace=None):
+    """Gradient of gated_linear_attn_fwd for the loss sum(dO * o) + sum(dS_T * S_T).
+    Returns dict(dq, dk, dv, dlog_alpha, dS0): dq, dk, dv of q's type (summed in
+    float32, rounded once), dlog_alpha (None when ungated) and dS0 float32."""
+    dev, dtype, (B, H, T), Dk, Dv = _recurrence_inputs(q, k, v, alpha, 4)
+    if dO is None:
+        raise TypeError("dO must be a torch.Tensor")
+    _need_shape(dO, "dO", (B, H, T, Dv), dtype, dev)
+    for t, n in ((S0, "S0"), (dS_T, "dS_T")):
+        _need_shape(t, n, (B, H, Dk, Dv), torch.float32, dev)
+    with torch.cuda.device(dev):
+        f = dict(dtype=torch.float32, device=dev)
+        out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
+                   dlog_alpha=None if alpha is None else torch.empty(B, H, T, **f),
+                   dS0=torch.empty(B, H, Dk, Dv, **f))
+        ws = workspace
+        if ws is None:
+            ws = _own_workspace(dev, _gated_bytes("gated_linear_attn_bwd_workspace_bytes", B, H, T, Dk, Dv, dtype))
+        _need(ws, "workspace", torch.uint8, dev)
+        check("gated_linear_attn_bwd", lib().gated_linear_attn_bwd(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(S0), _ptr(dO), _ptr(dS_T), _ptr(out["dq"]),
+            _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dlog_alpha"]), _ptr(out["dS0"]),
+            B, H, T, Dk, Dv, _DT[dtype], _ptr(ws), ws.numel(), _stream(dev)))
+    return out
+
+
+def gated_linear_attn_decode_step(q, k, v, S, alpha=None, o=None):
+    """One token of the gated linear recurrence for every cached state.  q, k:
+    (B,H,Dk); v: (B,H,Dv); alpha: (B,H) f32 or None; S: (B,H,Dk,Dv) f32, updated
+    in place.  Returns o (B,H,Dv) of q's type."""
+    dev, dtype, (B, H), Dk, Dv = _recurrence_inputs(q, k, v, alpha, 3)
+    if S is None:
+        raise TypeError("S must be a torch.Tensor")
+    _need_shape(S, "S", (B, H, Dk, Dv), torch.float32, dev)
+    with torch.cuda.device(dev):
+        if o is None:
+            o = torch.empty(B, H, Dv, dtype=dtype, device=dev)
+        _need_shape(o, "o", (B, H, Dv), dtype, dev)
+        check("gated_linear_attn_decode_step", lib().gated_linear_attn_decode_step(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(S), _ptr(o), B, H, Dk, Dv, _DT[dtype], _stream(dev)))
+    return o
+
+
+def _need_rows(t, name, dtype=None, device=None):
+    """A (B,T,H,D) tensor, strided, with contiguous rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must have 4 dimensions (B,T,H,D), got {t.dim()}")
+    if t.stride(3) != 1 and t.numel() > 0:
+        raise ValueError(f"{name} must have contiguous rows")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t
+
+
+def _row_strides(t):
+    """Strides over b, t and h; an axis of one element or none has stride 0."""
+    return [s if n > 1 else 0 for s, n in zip(t.stride()[:3], t.shape[:3])]
+
+
+def _qk_args(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, silu, interleaved):
+    _need_rows(q, "q")
+    dev, dtype = q.device, q.dtype
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype}")
+    _need_rows(k, "k", dtype, dev)
+    B, T, Hq, D = q.shape
+    Hk = k.shape[2]
+    if k.shape != (B, T, Hk, D):
+        raise ValueError(f"k must have shape {(B, T, 'Hk', D)}, got {tuple(k.shape)}")
+    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        _need_shape(t, n, (D,), torch.float32, dev)
+    pos_stride = 0
+    if positions is not None:
+        _need(positions, "positions", torch.int64, dev)
+        if positions.shape == (B, T):
+            pos_stride = T
+        elif positions.shape != (T,):
+            raise ValueError(f"positions must have shape {(B, T)} or {(T,)}, got {tuple(positions.shape)}")
+    rot = 0
+    if inv_freq is not None:
+        _need(inv_freq, "inv_freq", torch.float32, dev)
+        if inv_freq.dim() != 1:
+            raise ValueError(f"inv_freq must have one dimension, got {inv_freq.dim()}")
+        rot = 2 * inv_freq.shape[0]
+    if norm not in ("rms", "l2"):
+        raise ValueError(f'norm must be "rms" or "l2", got {norm!r}')
+    if eps is None:
+        eps = 1e-6 if norm == "rms" else 1e-12
+    opts = ((_lib.DN_QK_L2 if norm == "l2" else 0) | (_lib.DN_QK_SILU if silu else 0)
+            | (_lib.DN_QK_INTERLEAVED if interleaved else 0))
+    return dev, dtype, B, T, Hq, Hk, D, rot, pos_stride, float(eps), opts
+
+
+def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None, norm: str = "rms",
+                     eps=None, silu: bool = False, interleaved: bool = False, q_out=None, k_out=None):
+    """Per-head norm of queries and keys and their rotation by position.
+    q: (B,T,Hq,D), k: (B,T,Hk,D), strided views with contiguous rows (bf16 or
+    f32, bases and strides multiples of 16 bytes); weights: (D,) f32 or None;
+    positions: (B,T) or (T,) int64, None for 0..T-1; inv_freq: (rot/2,) f32,
+    None for no rotation; norm: "rms" (eps 1e-6 inside the root) or "l2" (the
+    norm at least eps, 1e-12); ``silu``: the feature map in front of the norm;
+    ``interleaved``: pairs (2i, 2i+1) instead of (i, i + rot/2).  Returns
+    (B,Hq,T,D) and (B,Hk,T,D), contiguous: what the mixing calls take."""
+    dev, dtype, B, T, Hq, Hk, D, rot, ps, eps, opts = _qk_args(
+        q, k, q_weight, k_weight, positions, inv_freq, norm, eps, silu, interleaved)
+    with torch.cuda.device(dev):
+        if q_out is None:
+            q_out = torch.empty(B, Hq, T, D, dtype=dtype, device=dev)
+        if k_out is None:
+            k_out = torch.empty(B, Hk, T, D, dtype=dtype, device=dev)
+        _need_shape(q_out, "q_out", (B, Hq, T, D), dtype, dev)
+        _need_shape(k_out, "k_out", (B, Hk, T, D), dtype, dev)
+        check("qk_norm_rope_fwd", lib().qk_norm_rope_fwd(
+            _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), _ptr(q_out),
+            _ptr(k_out), B, T, Hq, Hk, D, rot, *_row_strides(q), *_row_strides(k), ps, eps, opts, _DT[dtype],
+            _stream(dev)))
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, positions=None, inv_freq=None,
+                     norm: str = "rms", eps=None, silu: bool = False, interleaved: bool = False, dq=None, dk=None,
+                     workspace=None):
+    """Gradient of qk_norm_rope_fwd.  dq_out: (B,Hq,T,D) and dk_out: (B,Hk,T,D),
+    both of q's type or both float32; dq, dk: where to write the derivatives by q and k
+    ((B,T,H,D) views like q and k, slices of one fused gradient, say; new
+    tensors if None).  Returns dict(dq, dk, dq_weight, dk_weight), the weights'
+    derivatives (D,) float32, None for a weight that is None."""
+    dev, dtype, B, T, Hq, Hk, D, rot, ps, eps, opts = _qk_args(
+        q, k, q_weight, k_weight, positions, inv_freq, norm, eps, silu, interleaved)
+    if not isinstance(dq_out, torch.Tensor) or not isinstance(dk_out, torch.Tensor):
+        raise TypeError("dq_out and dk_out must be torch.Tensors")
+    gdt = dq_out.dtype
+    if gdt not in (dtype, torch.float32):
+        raise TypeError(f"dq_out must be {dtype} or torch.float32, got {gdt}")
+    _need_shape(dq_out, "dq_out", (B, Hq, T, D), gdt, dev)
+    _need_shape(dk_out, "dk_out", (B, Hk, T, D), gdt, dev)
+    with torch.cuda.device(dev):
+        if dq is None:
+            dq = torch.empty(B, T, Hq, D, dtype=dtype, device=dev)
+        if dk is None:
+            dk = torch.empty(B, T, Hk, D, dtype=dtype, device=dev)
+        for t, n, like in ((dq, "dq", q), (dk, "dk", k)):
+            _need_rows(t, n, dtype, dev)
+            if t.shape != like.shape:
+                raise ValueError(f"{n} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
+        dw = [None if w is None else torch.empty(D, dtype=torch.float32, device=dev) for w in (q_weight, k_weight)]
+        ws = workspace
+        if ws is None and (q_weight is not None or k_weight is not None):
+            nb = lib().qk_norm_rope_bwd_workspace_bytes(B, T, Hq, Hk, D)
+            if nb == 0:
+                raise DeltaNetError("qk_norm_rope_bwd_workspace_bytes", _lib.DN_ERR_UNSUPPORTED)
+            ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+        if ws is not None:
+            _need(ws, "workspace", torch.uint8, dev)
+        check("qk_norm_rope_bwd", lib().qk_norm_rope_bwd(
+            _ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
+            _ptr(inv_freq), _ptr(dq), _ptr(dk), _ptr(dw[0]), _ptr(dw[1]), B, T, Hq, Hk, D, rot,
+            *_row_strides(q), *_row_strides(k), *_row_strides(dq), *_row_strides(dk), ps, eps, opts, _DT[dtype],
+            _DT[gdt], _ptr(ws), 0 if ws is None else ws.numel(), _stream(dev)))
+    return dict(dq=dq, dk=dk, dq_weight=dw[0], dk_weight=dw[1])
 
 
 def deltanet_get_device_status(device=None, workspace=None) -> int:

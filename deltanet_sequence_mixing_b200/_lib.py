@@ -20,11 +20,13 @@ DN_ERR_CUDA = -4
 DN_ERR_DEVICE_TIMEOUT = -5
 DN_ERR_WORKSPACE = -6
 DN_F32, DN_BF16 = 0, 1
+DN_QK_L2, DN_QK_SILU, DN_QK_INTERLEAVED = 1, 2, 4
 DN_OPT_PRESTEP, DN_OPT_GATE_PER_DIM, DN_OPT_SEQ_SPLIT = 1, 2, 4
 
 # Every symbol include/deltanet.h declares, with (restype, argtypes).
 _vp, _sz, _i, _ll, _u = (ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_longlong,
                          ctypes.c_uint)
+_f = ctypes.c_float
 SIGNATURES = {
     "deltanet_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "deltanet_workspace_init": (_i, [_vp, _sz, _vp]),
@@ -49,6 +51,14 @@ SIGNATURES = {
     "deltanet_chunk_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                 _vp, _vp, _vp, _vp, _vp, _vp,
                                 _i, _i, _i, _i, _i, _i, _vp, _sz, _vp]),
+    "gated_linear_attn_workspace_bytes": (_sz, [_i] * 6),
+    "gated_linear_attn_fwd": (_i, [_vp] * 7 + [_i] * 6 + [_vp, _sz, _vp]),
+    "gated_linear_attn_bwd_workspace_bytes": (_sz, [_i] * 6),
+    "gated_linear_attn_bwd": (_i, [_vp] * 12 + [_i] * 6 + [_vp, _sz, _vp]),
+    "gated_linear_attn_decode_step": (_i, [_vp] * 6 + [_i] * 5 + [_vp]),
+    "qk_norm_rope_fwd": (_i, [_vp] * 8 + [_i] * 6 + [_ll] * 7 + [_f, _u, _i, _vp]),
+    "qk_norm_rope_bwd_workspace_bytes": (_sz, [_i] * 5),
+    "qk_norm_rope_bwd": (_i, [_vp] * 12 + [_i] * 6 + [_ll] * 13 + [_f, _u, _i, _i, _vp, _sz, _vp]),
     "deltanet_get_device_status": (_i, [_vp, _vp]),
     "deltanet_selftest_wait_timeout": (_i, [_vp, _sz, _ll, _vp]),
     "deltanet_status_string": (ctypes.c_char_p, [_i]),

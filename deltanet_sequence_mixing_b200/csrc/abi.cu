@@ -347,9 +347,318 @@ int run_split(dn::ChunkProblem& p, int G, void* ws, cudaStream_t st) {
   return map_cuda(e);
 }
 
+// ------------------------------------------------ gated linear recurrence --
+int validate_gated_sizes(int B, int H, int T, int Dk, int Dv, int dt) {
+  if (dt != DN_F32 && dt != DN_BF16) return DN_ERR_UNSUPPORTED;
+  if (B < 0 || H < 0 || T < 0) return DN_ERR_INVALID_ARG;
+  if (!valid_dim(Dk) || !valid_dim(Dv)) return DN_ERR_UNSUPPORTED;
+  // one CTA per (b, h, 32-column slice of Dv) or per (b, h, chunk) on a
+  // one-dimensional grid
+  const long long BH = (long long)B * H;
+  if (BH > INT_MAX / 4) return DN_ERR_UNSUPPORTED;
+  if (BH * (((long long)T + dn::kGatedSimtChunk - 1) / dn::kGatedSimtChunk) > INT_MAX) return DN_ERR_UNSUPPORTED;
+  return DN_OK;
+}
+
+// The state of the sequence's end when there are no tokens.
+int carry_state(float* dst, const float* src, size_t bytes, cudaStream_t st) {
+  if (!dst || dst == src || bytes == 0) return DN_OK;
+  return map_cuda(src ? cudaMemcpyAsync(dst, src, bytes, cudaMemcpyDeviceToDevice, st)
+                      : cudaMemsetAsync(dst, 0, bytes, st));
+}
+
+// DN_OK if no output (with its byte range) overlaps an input or another output.
+template <size_t NI, size_t NO>
+int disjoint(const Range (&ins)[NI], const Range (&outs)[NO]) {
+  for (size_t a = 0; a < NO; ++a) {
+    for (const Range& r : ins)
+      if (overlap(outs[a], r)) return DN_ERR_INVALID_ARG;
+    for (size_t b = a + 1; b < NO; ++b)
+      if (overlap(outs[a], outs[b])) return DN_ERR_INVALID_ARG;
+  }
+  return DN_OK;
+}
+
+// ---------------------------------------------------- q/k norm and rotation --
+constexpr unsigned int kKnownQkOptions = DN_QK_L2 | DN_QK_SILU | DN_QK_INTERLEAVED;
+
+// Sizes, options and the strided inputs of both directions.
+int validate_qk(const dn::QkProblem& p, unsigned int options) {
+  if (options & ~kKnownQkOptions) return DN_ERR_INVALID_ARG;
+  if (p.B < 0 || p.T < 0 || p.Hq < 0 || p.Hk < 0) return DN_ERR_INVALID_ARG;
+  if (!valid_dim(p.D) || p.rot < 0 || p.rot > p.D || p.rot % 16 != 0) return DN_ERR_UNSUPPORTED;
+  if (!(p.eps > 0.f) || p.eps > 3.4e38f) return DN_ERR_INVALID_ARG;
+  const long long N = (long long)p.B * p.T, heads = (long long)p.Hq + p.Hk;
+  // CTAs of at least one token; 16 tokens times the heads stay in an int
+  if (N > INT_MAX || heads > INT_MAX / 16) return DN_ERR_UNSUPPORTED;
+  for (long long s : {p.qs_b, p.qs_t, p.qs_h, p.ks_b, p.ks_t, p.ks_h, p.pos_stride_b})
+    if (s < 0) return DN_ERR_INVALID_ARG;
+  if (N == 0) return DN_OK;
+  if ((p.Hq > 0 && !p.q) || (p.Hk > 0 && !p.k)) return DN_ERR_INVALID_ARG;
+  if (p.rot > 0 && heads > 0 && !p.inv_freq) return DN_ERR_INVALID_ARG;
+  const long long per16 = p.bf16 ? 8 : 4;  // elements of 16 bytes
+  if (p.Hq > 0 && (!aligned16(p.q) || p.qs_b % per16 || p.qs_t % per16 || p.qs_h % per16)) return DN_ERR_ALIGNMENT;
+  if (p.Hk > 0 && (!aligned16(p.k) || p.ks_b % per16 || p.ks_t % per16 || p.ks_h % per16)) return DN_ERR_ALIGNMENT;
+  for (const void* x : {(const void*)p.q_weight, (const void*)p.k_weight, (const void*)p.inv_freq})
+    if (reinterpret_cast<uintptr_t>(x) & 3u) return DN_ERR_ALIGNMENT;
+  if (reinterpret_cast<uintptr_t>(p.positions) & 7u) return DN_ERR_ALIGNMENT;
+  return DN_OK;
+}
+
+// Bytes from the base to the end of the last row of a strided tensor.
+size_t span(int B, int T, int H, int D, long long sb, long long st, long long sh, size_t es) {
+  if (B == 0 || T == 0 || H == 0) return 0;
+  return ((size_t)(B - 1) * sb + (size_t)(T - 1) * st + (size_t)(H - 1) * sh + D) * es;
+}
+
+// True if no two rows of a strided output share an element: with the axes in
+// the order of their strides, each stride is at least the extent below it.
+bool rows_apart(int B, int T, int H, int D, long long sb, long long st, long long sh) {
+  struct Axis {
+    long long stride, n;
+  } ax[3] = {{sb, B}, {st, T}, {sh, H}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (ax[j].stride < ax[i].stride) {
+        const Axis x = ax[i];
+        ax[i] = ax[j];
+        ax[j] = x;
+      }
+  long long extent = D;
+  for (const Axis& a : ax) {
+    if (a.n <= 1) continue;
+    if (a.stride < extent) return false;
+    extent += a.stride * (a.n - 1);
+  }
+  return true;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t gated_linear_attn_workspace_bytes(int B, int H, int T, int Dk, int Dv, dn_dtype dt) {
+  if (validate_gated_sizes(B, H, T, Dk, Dv, dt) != DN_OK) return 0;
+  return kStatusBytes;
+}
+
+int gated_linear_attn_fwd(const void* q, const void* k, const void* v, const float* alpha, const float* S0, void* o,
+                          float* S_out, int B, int H, int T, int Dk, int Dv, dn_dtype dt, void* workspace,
+                          size_t ws_bytes, void* cuda_stream) {
+  int rc = validate_gated_sizes(B, H, T, Dk, Dv, dt);
+  if (rc != DN_OK) return rc;
+  // empty tensors may carry null pointers
+  if ((long long)B * H > 0 && T > 0 && (!q || !k || !v || !o)) return DN_ERR_INVALID_ARG;
+  if (!workspace) return DN_ERR_WORKSPACE;
+  if (ws_bytes < gated_linear_attn_workspace_bytes(B, H, T, Dk, Dv, dt)) return DN_ERR_WORKSPACE;
+  for (const void* x : {q, k, v, (const void*)o, (const void*)S0, (const void*)S_out, (const void*)workspace})
+    if (!aligned16(x)) return DN_ERR_ALIGNMENT;
+  if (reinterpret_cast<uintptr_t>(alpha) & 3u) return DN_ERR_ALIGNMENT;
+  const size_t es = dt == DN_BF16 ? 2 : 4, BH = (size_t)B * H, N = BH * T, nS = BH * Dk * Dv * 4;
+  const Range ins[] = {range_of(q, N * Dk * es), range_of(k, N * Dk * es), range_of(v, N * Dv * es),
+                       range_of(alpha, alpha ? N * 4 : 0), range_of(S0, S0 && S0 != S_out ? nS : 0)};
+  const Range outs[] = {range_of(o, N * Dv * es), range_of(S_out, S_out ? nS : 0), range_of(workspace, ws_bytes)};
+  rc = disjoint(ins, outs);
+  if (rc != DN_OK) return rc;
+  if (BH == 0) return DN_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if (T == 0) return carry_state(S_out, S0, nS, st);
+  dn::GatedProblem p{};
+  p.q = q; p.k = k; p.v = v; p.alpha = alpha; p.S0 = S0; p.o = o; p.S_out = S_out;
+  p.B = B; p.H = H; p.T = T; p.Dk = Dk; p.Dv = Dv;
+  p.bf16 = dt == DN_BF16;
+  p.status = static_cast<unsigned int*>(workspace);
+  p.scratch = static_cast<uint8_t*>(workspace) + kStatusBytes;
+  return map_cuda(dn::launch_gated_simt_fwd(p, st));
+}
+
+size_t gated_linear_attn_bwd_workspace_bytes(int B, int H, int T, int Dk, int Dv, dn_dtype dt) {
+  if (validate_gated_sizes(B, H, T, Dk, Dv, dt) != DN_OK) return 0;
+  const size_t chunks = ((size_t)T + dn::kGatedSimtChunk - 1) / dn::kGatedSimtChunk;
+  return kStatusBytes + 2 * (size_t)B * H * chunks * Dk * Dv * 4;
+}
+
+int gated_linear_attn_bwd(const void* q, const void* k, const void* v, const float* alpha, const float* S0,
+                          const void* dO, const float* dS_T, void* dq, void* dk, void* dv, float* dlog_alpha,
+                          float* dS0, int B, int H, int T, int Dk, int Dv, dn_dtype dt, void* workspace,
+                          size_t ws_bytes, void* cuda_stream) {
+  int rc = validate_gated_sizes(B, H, T, Dk, Dv, dt);
+  if (rc != DN_OK) return rc;
+  if ((long long)B * H > 0 && T > 0 && (!q || !k || !v || !dO || !dq || !dk || !dv)) return DN_ERR_INVALID_ARG;
+  if (dlog_alpha && !alpha) return DN_ERR_INVALID_ARG;
+  if (!workspace) return DN_ERR_WORKSPACE;
+  if (ws_bytes < gated_linear_attn_bwd_workspace_bytes(B, H, T, Dk, Dv, dt)) return DN_ERR_WORKSPACE;
+  for (const void* x : {q, k, v, dO, (const void*)dq, (const void*)dk, (const void*)dv, (const void*)S0,
+                        (const void*)dS_T, (const void*)dS0, (const void*)workspace})
+    if (!aligned16(x)) return DN_ERR_ALIGNMENT;
+  for (const void* x : {(const void*)alpha, (const void*)dlog_alpha})
+    if (reinterpret_cast<uintptr_t>(x) & 3u) return DN_ERR_ALIGNMENT;
+  const size_t es = dt == DN_BF16 ? 2 : 4, BH = (size_t)B * H, N = BH * T, nS = BH * Dk * Dv * 4;
+  const Range ins[] = {range_of(q, N * Dk * es),           range_of(k, N * Dk * es),
+                       range_of(v, N * Dv * es),           range_of(dO, N * Dv * es),
+                       range_of(alpha, alpha ? N * 4 : 0), range_of(S0, S0 ? nS : 0),
+                       range_of(dS_T, dS_T ? nS : 0)};
+  const Range outs[] = {range_of(dq, N * Dk * es),
+                        range_of(dk, N * Dk * es),
+                        range_of(dv, N * Dv * es),
+                        range_of(dlog_alpha, dlog_alpha ? N * 4 : 0),
+                        range_of(dS0, dS0 ? nS : 0),
+                        range_of(workspace, ws_bytes)};
+  rc = disjoint(ins, outs);
+  if (rc != DN_OK) return rc;
+  if (BH == 0) return DN_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if (T == 0) return carry_state(dS0, dS_T, nS, st);
+  dn::GatedProblem p{};
+  p.q = q; p.k = k; p.v = v; p.alpha = alpha; p.S0 = S0; p.dO = dO; p.dS_T = dS_T;
+  p.dq = dq; p.dk = dk; p.dv = dv; p.dlog_alpha = dlog_alpha; p.dS0 = dS0;
+  p.B = B; p.H = H; p.T = T; p.Dk = Dk; p.Dv = Dv;
+  p.bf16 = dt == DN_BF16;
+  p.status = static_cast<unsigned int*>(workspace);
+  p.scratch = static_cast<uint8_t*>(workspace) + kStatusBytes;
+  return map_cuda(dn::launch_gated_simt_bwd(p, st));
+}
+
+int gated_linear_attn_decode_step(const void* q, const void* k, const void* v, const float* alpha, float* S, void* o,
+                                  int B, int H, int Dk, int Dv, dn_dtype dt, void* cuda_stream) {
+  int rc = validate_gated_sizes(B, H, 1, Dk, Dv, dt);
+  if (rc != DN_OK) return rc;
+  const size_t es = dt == DN_BF16 ? 2 : 4, BH = (size_t)B * H;
+  if (BH == 0) return DN_OK;  // empty tensors may carry null pointers
+  if (!q || !k || !v || !S || !o) return DN_ERR_INVALID_ARG;
+  for (const void* x : {q, k, v, (const void*)S, (const void*)o})
+    if (!aligned16(x)) return DN_ERR_ALIGNMENT;
+  if (reinterpret_cast<uintptr_t>(alpha) & 3u) return DN_ERR_ALIGNMENT;
+  const Range ins[] = {range_of(q, BH * Dk * es), range_of(k, BH * Dk * es), range_of(v, BH * Dv * es),
+                       range_of(alpha, alpha ? BH * 4 : 0)};
+  const Range outs[] = {range_of(S, BH * Dk * Dv * 4), range_of(o, BH * Dv * es)};
+  rc = disjoint(ins, outs);
+  if (rc != DN_OK) return rc;
+  const dn::GatedStepProblem p{q, k, v, alpha, S, o, B, H, Dk, Dv, dt == DN_BF16};
+  return map_cuda(dn::launch_gated_step(p, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+int qk_norm_rope_fwd(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                     const long long* positions, const float* inv_freq, void* q_out, void* k_out, int B, int T,
+                     int Hq, int Hk, int D, int rot, long long qs_b, long long qs_t, long long qs_h, long long ks_b,
+                     long long ks_t, long long ks_h, long long pos_stride_b, float eps, unsigned int options,
+                     dn_dtype dt, void* cuda_stream) {
+  if (dt != DN_F32 && dt != DN_BF16) return DN_ERR_UNSUPPORTED;
+  dn::QkProblem p{};
+  p.q = q; p.k = k; p.q_weight = q_weight; p.k_weight = k_weight; p.positions = positions; p.inv_freq = inv_freq;
+  p.q_out = q_out; p.k_out = k_out;
+  p.B = B; p.T = T; p.Hq = Hq; p.Hk = Hk; p.D = D; p.rot = rot;
+  p.qs_b = qs_b; p.qs_t = qs_t; p.qs_h = qs_h; p.ks_b = ks_b; p.ks_t = ks_t; p.ks_h = ks_h;
+  p.pos_stride_b = pos_stride_b;
+  p.eps = eps;
+  p.l2 = (options & DN_QK_L2) != 0;
+  p.silu = (options & DN_QK_SILU) != 0;
+  p.interleaved = (options & DN_QK_INTERLEAVED) != 0;
+  p.bf16 = dt == DN_BF16;
+  int rc = validate_qk(p, options);
+  if (rc != DN_OK) return rc;
+  const size_t es = p.bf16 ? 2 : 4, N = (size_t)B * T;
+  if (N == 0 || Hq + Hk == 0) return DN_OK;
+  if ((Hq > 0 && !q_out) || (Hk > 0 && !k_out)) return DN_ERR_INVALID_ARG;
+  if ((Hq > 0 && !aligned16(q_out)) || (Hk > 0 && !aligned16(k_out))) return DN_ERR_ALIGNMENT;
+  const Range ins[] = {range_of(q, span(B, T, Hq, D, qs_b, qs_t, qs_h, es)),
+                       range_of(k, span(B, T, Hk, D, ks_b, ks_t, ks_h, es)),
+                       range_of(q_weight, q_weight ? (size_t)D * 4 : 0),
+                       range_of(k_weight, k_weight ? (size_t)D * 4 : 0),
+                       range_of(positions, positions ? ((size_t)(B - 1) * pos_stride_b + T) * 8 : 0),
+                       range_of(inv_freq, inv_freq ? (size_t)rot * 2 : 0)};
+  const Range outs[] = {range_of(q_out, N * Hq * D * es), range_of(k_out, N * Hk * D * es)};
+  rc = disjoint(ins, outs);
+  if (rc != DN_OK) return rc;
+  return map_cuda(dn::launch_qk_fwd(p, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+size_t qk_norm_rope_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int D) {
+  if (B < 0 || T < 0 || Hq < 0 || Hk < 0 || !valid_dim(D) || (long long)B * T > INT_MAX ||
+      (long long)Hq + Hk > INT_MAX / 16)
+    return 0;
+  if (B == 0 || T == 0 || Hq + Hk == 0) return 16;  // nothing to add up, still a buffer
+  return (size_t)dn::qk_bwd_ctas(B, T, Hq, Hk) * 2 * D * 4;
+}
+
+int qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, const float* q_weight,
+                     const float* k_weight, const long long* positions, const float* inv_freq, void* dq, void* dk,
+                     float* dq_weight, float* dk_weight, int B, int T, int Hq, int Hk, int D, int rot, long long qs_b,
+                     long long qs_t, long long qs_h, long long ks_b, long long ks_t, long long ks_h, long long dqs_b,
+                     long long dqs_t, long long dqs_h, long long dks_b, long long dks_t, long long dks_h,
+                     long long pos_stride_b, float eps, unsigned int options, dn_dtype dt, dn_dtype grad_dt,
+                     void* workspace, size_t ws_bytes, void* cuda_stream) {
+  if (dt != DN_F32 && dt != DN_BF16) return DN_ERR_UNSUPPORTED;
+  if (grad_dt != dt && grad_dt != DN_F32) return DN_ERR_UNSUPPORTED;
+  dn::QkProblem p{};
+  p.q = q; p.k = k; p.q_weight = q_weight; p.k_weight = k_weight; p.positions = positions; p.inv_freq = inv_freq;
+  p.q_out = dq; p.k_out = dk; p.dq_in = dq_out; p.dk_in = dk_out;
+  p.dq_weight = dq_weight; p.dk_weight = dk_weight;
+  p.B = B; p.T = T; p.Hq = Hq; p.Hk = Hk; p.D = D; p.rot = rot;
+  p.qs_b = qs_b; p.qs_t = qs_t; p.qs_h = qs_h; p.ks_b = ks_b; p.ks_t = ks_t; p.ks_h = ks_h;
+  p.dqs_b = dqs_b; p.dqs_t = dqs_t; p.dqs_h = dqs_h; p.dks_b = dks_b; p.dks_t = dks_t; p.dks_h = dks_h;
+  p.pos_stride_b = pos_stride_b;
+  p.eps = eps;
+  p.l2 = (options & DN_QK_L2) != 0;
+  p.silu = (options & DN_QK_SILU) != 0;
+  p.interleaved = (options & DN_QK_INTERLEAVED) != 0;
+  p.bf16 = dt == DN_BF16;
+  p.grad_bf16 = grad_dt == DN_BF16;
+  int rc = validate_qk(p, options);
+  if (rc != DN_OK) return rc;
+  if ((dq_weight && !q_weight) || (dk_weight && !k_weight)) return DN_ERR_INVALID_ARG;
+  for (long long s : {dqs_b, dqs_t, dqs_h, dks_b, dks_t, dks_h})
+    if (s < 0) return DN_ERR_INVALID_ARG;
+  const size_t es = p.bf16 ? 2 : 4, ges = p.grad_bf16 ? 2 : 4, N = (size_t)B * T;
+  const bool rows = N > 0 && Hq + Hk > 0, weights = dq_weight || dk_weight;
+  if (rows) {
+    if ((Hq > 0 && (!dq || !dq_out)) || (Hk > 0 && (!dk || !dk_out))) return DN_ERR_INVALID_ARG;
+    const long long per16 = p.bf16 ? 8 : 4;
+    if (Hq > 0 && (!aligned16(dq) || !aligned16(dq_out) || dqs_b % per16 || dqs_t % per16 || dqs_h % per16))
+      return DN_ERR_ALIGNMENT;
+    if (Hk > 0 && (!aligned16(dk) || !aligned16(dk_out) || dks_b % per16 || dks_t % per16 || dks_h % per16))
+      return DN_ERR_ALIGNMENT;
+    if (!rows_apart(B, T, Hq, D, dqs_b, dqs_t, dqs_h) || !rows_apart(B, T, Hk, D, dks_b, dks_t, dks_h))
+      return DN_ERR_INVALID_ARG;
+  }
+  for (const void* x : {(const void*)dq_weight, (const void*)dk_weight})
+    if (reinterpret_cast<uintptr_t>(x) & 3u) return DN_ERR_ALIGNMENT;
+  if (weights) {
+    if (!workspace || ws_bytes < qk_norm_rope_bwd_workspace_bytes(B, T, Hq, Hk, D)) return DN_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return DN_ERR_ALIGNMENT;
+  }
+  const size_t sq = span(B, T, Hq, D, dqs_b, dqs_t, dqs_h, es), sk = span(B, T, Hk, D, dks_b, dks_t, dks_h, es);
+  const Range ins[] = {range_of(q, span(B, T, Hq, D, qs_b, qs_t, qs_h, es)),
+                       range_of(k, span(B, T, Hk, D, ks_b, ks_t, ks_h, es)),
+                       range_of(dq_out, N * Hq * D * ges),
+                       range_of(dk_out, N * Hk * D * ges),
+                       range_of(q_weight, q_weight ? (size_t)D * 4 : 0),
+                       range_of(k_weight, k_weight ? (size_t)D * 4 : 0),
+                       range_of(positions, rows && positions ? ((size_t)(B - 1) * pos_stride_b + T) * 8 : 0),
+                       range_of(inv_freq, inv_freq ? (size_t)rot * 2 : 0)};
+  const size_t nw = (size_t)D * 4;
+  const Range rest[] = {range_of(dq_weight, dq_weight ? nw : 0), range_of(dk_weight, dk_weight ? nw : 0),
+                        range_of(workspace, weights ? ws_bytes : 0)};
+  rc = disjoint(ins, rest);
+  // dq and dk: apart from the rest, but they may be slices of one fused
+  // gradient, and q, k slices of the projection beside it
+  for (const Range& r : {range_of(dq, rows ? sq : 0), range_of(dk, rows ? sk : 0)}) {
+    for (const Range& x : ins)
+      if (rc == DN_OK && overlap(r, x)) rc = DN_ERR_INVALID_ARG;
+    for (const Range& x : rest)
+      if (rc == DN_OK && overlap(r, x)) rc = DN_ERR_INVALID_ARG;
+  }
+  if (rc != DN_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if (!rows) {  // sums over nothing
+    cudaError_t e = cudaSuccess;
+    if (dq_weight) e = cudaMemsetAsync(dq_weight, 0, nw, st);
+    if (e == cudaSuccess && dk_weight) e = cudaMemsetAsync(dk_weight, 0, nw, st);
+    return map_cuda(e);
+  }
+  p.partial = weights ? static_cast<float*>(workspace) : nullptr;
+  return map_cuda(dn::launch_qk_bwd(p, st));
+}
 
 int deltanet_seq_segments(int B, int H, int T, int Dk, int Dv, int C, dn_dtype dt, unsigned int options) {
   return seq_segments(B, H, T, Dk, Dv, C, dt, options);

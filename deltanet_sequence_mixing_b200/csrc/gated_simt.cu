@@ -1,0 +1,429 @@
+// Gated linear recurrence on CUDA cores (float32 arithmetic): forward and
+// gradient.  Per (b, h), with a Dk x Dv state,
+//     S_t = alpha_t S_{t-1} + k_t^T v_t,   o_t = q_t S_t.
+//
+// Chunks of C = 32 tokens entered with S.  With D_ij the product of alpha over
+// (j, i], G_i the product over [0, i], c_j the product over (j, C) and gamma
+// the product over the chunk (tokens past T count as alpha = 1, q = k = v = 0):
+//   forward   O = diag(G) Q S + (tril(Q K^T) * D) V,   S <- gamma S + K^T diag(c) V
+//   reverse   R <- gamma R + Q^T diag(G) dO            (R: the loss's derivative by S)
+//   gradient  A = tril(Q K^T) * D, B = tril(dO V^T) * D
+//             dQ = B K + diag(G) dO S^T
+//             dK = B^T Q + diag(c) V R^T,   dV = A^T dO + diag(c) K R
+// The decays are running products of alpha, never exponentials of sums of
+// logarithms: a hard wipe (alpha = 0) is exact, and D_ij keeps its relative
+// accuracy however strongly the chunk as a whole decays.
+//
+// The gradient of log alpha_t is the sum of all paths from a write before t to
+// a read at or after it:
+//   sum_{i >= t > j} M_ij + sum_{i >= t} r_i + sum_{j < t} e_j + gamma <S, R>
+//   M = (Q K^T) * (dO V^T) * D,  r_i = q_i . (G_i dO_i S^T),  e_j = k_j . (c_j v_j R^T)
+// where the first term is the suffix sum of (row sum - column sum) of M below
+// its diagonal.  Sums stay inside one chunk, so no error travels along T.
+//
+// Three kernels: the state scan (forward, or reverse with (q, dO) in the place
+// of (k, v); one CTA per (b, h, 32 columns of Dv), serial over chunks), which
+// stores each chunk's entry state when the gradient needs it, and the gradient
+// of every chunk side by side.
+#include <cuda_bf16.h>
+
+#include "kernels.h"
+
+namespace dn {
+namespace {
+
+constexpr int C = kGatedSimtChunk, kThreads = 256, NV = 32, CP = C + 1;
+static_assert(C == 32, "one lane per token of a chunk");
+
+template <typename TI>
+__device__ __forceinline__ float ld(const TI* p, size_t i);
+template <>
+__device__ __forceinline__ float ld<float>(const float* p, size_t i) { return p[i]; }
+template <>
+__device__ __forceinline__ float ld<__nv_bfloat16>(const __nv_bfloat16* p, size_t i) {
+  return __bfloat162float(p[i]);
+}
+__device__ __forceinline__ void st(float* p, size_t i, float x) { p[i] = x; }
+__device__ __forceinline__ void st(__nv_bfloat16* p, size_t i, float x) { p[i] = __float2bfloat16_rn(x); }
+
+// acc[x][y] += sum_{k < nk} A[(r0 + 16 x) ars + k acs] B[k brs + (c0 + 16 y) bcs]
+// for thread (r0, c0) of the CTA's 16 x 16 grid.
+template <int RX, int RY>
+__device__ __forceinline__ void product(int nk, const float* A, int ars, int acs, const float* B, int brs, int bcs,
+                                        float (&acc)[RX][RY]) {
+  const int r0 = threadIdx.x >> 4, c0 = threadIdx.x & 15;
+#pragma unroll 4
+  for (int k = 0; k < nk; ++k) {
+    float a[RX], b[RY];
+#pragma unroll
+    for (int x = 0; x < RX; ++x) a[x] = A[(r0 + 16 * x) * ars + k * acs];
+#pragma unroll
+    for (int y = 0; y < RY; ++y) b[y] = B[k * brs + (c0 + 16 * y) * bcs];
+#pragma unroll
+    for (int x = 0; x < RX; ++x)
+#pragma unroll
+      for (int y = 0; y < RY; ++y) acc[x][y] = fmaf(a[x], b[y], acc[x][y]);
+  }
+}
+
+// One warp: the chunk's decays from alpha (n tokens; 1 behind them).
+// into[i] = G_i, out[j] = c_j, D (if not null) the C x C matrix of D_ij, zero
+// above the diagonal.  Returns gamma.
+__device__ __forceinline__ float chunk_decays(const float* alpha, int n, float* into, float* out, float* D) {
+  const int lane = threadIdx.x & 31;
+  const float a = alpha && lane < n ? alpha[lane] : 1.f;
+  float pre = a;                                             // product over [0, lane]
+  float suf = __shfl_down_sync(0xffffffffu, a, 1);           // product over (lane, C)
+  if (lane == 31) suf = 1.f;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float x = __shfl_up_sync(0xffffffffu, pre, o), y = __shfl_down_sync(0xffffffffu, suf, o);
+    if (lane >= o) pre *= x;
+    if (lane + o < 32) suf *= y;
+  }
+  into[lane] = pre;
+  out[lane] = suf;
+  if (D) {
+    float d = 0.f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const float ai = __shfl_sync(0xffffffffu, a, i);
+      d = i == lane ? 1.f : d * ai;
+      D[i * CP + lane] = i < lane ? 0.f : d;
+    }
+  }
+  return __shfl_sync(0xffffffffu, pre, 31);
+}
+
+// ------------------------------------------------------------------- scan --
+// Forward: x = k, z = v, S <- gamma S + K^T diag(c) V, and o if OUT.
+// Reverse: x = q, z = dO, chunks from the last, R <- gamma R + Q^T diag(G) dO.
+// `states` (if not null) takes the state that each chunk is entered with, in
+// the scan's own direction.
+template <typename TI, int DK, bool REV, bool OUT>
+__global__ void __launch_bounds__(kThreads) gated_simt_scan_kernel(const GatedProblem p, float* states) {
+  constexpr int KP = DK + 1, VP = NV + 1, RK = DK / 16;
+  __shared__ float into[C], out[C], gam;
+  extern __shared__ float sm[];
+  float* Xs = sm;               // C x KP: k (forward), q (reverse)
+  float* Zs = Xs + C * KP;      // C x VP: v (forward), dO (reverse)
+  float* Ss = Zs + C * VP;      // DK x VP
+  float* Qs = Ss + DK * VP;     // C x KP (OUT)
+  float* Ps = Qs + C * KP;      // C x CP (OUT)
+  float* Ds = Ps + C * CP;      // C x CP (OUT)
+  const int tid = threadIdx.x, r0 = tid >> 4, c0 = tid & 15;
+  const int T = p.T, Dv = p.Dv, nch = (T + C - 1) / C, nsl = Dv / NV;
+  const size_t bh = blockIdx.x / nsl;
+  const int j0 = (int)(blockIdx.x % nsl) * NV;
+  const size_t sblk = (size_t)DK * Dv;
+  const TI* x = static_cast<const TI*>(REV ? p.q : p.k) + bh * T * DK;
+  const TI* q = static_cast<const TI*>(p.q) + bh * T * DK;
+  const TI* z = static_cast<const TI*>(REV ? p.dO : p.v) + bh * T * Dv + j0;
+  TI* o = OUT ? static_cast<TI*>(p.o) + bh * T * Dv + j0 : nullptr;
+  const float* alpha = p.alpha ? p.alpha + bh * T : nullptr;
+  const float* S_in = REV ? p.dS_T : p.S0;
+  float* S_end = REV ? p.dS0 : p.S_out;
+
+  float s[RK][2];  // this thread's rows r0 + 16 x, columns c0 + 16 y of the state
+#pragma unroll
+  for (int xx = 0; xx < RK; ++xx)
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+      s[xx][y] = S_in ? S_in[bh * sblk + (size_t)(r0 + 16 * xx) * Dv + j0 + c0 + 16 * y] : 0.f;
+
+  for (int cc = 0; cc < nch; ++cc) {
+    const int c = REV ? nch - 1 - cc : cc, t0 = c * C, n = min(C, T - t0);
+    __syncthreads();  // the products of the chunk before have read the tiles
+    for (int i = tid; i < C * DK; i += kThreads) {
+      const int r = i / DK, d = i % DK;
+      Xs[r * KP + d] = r < n ? ld(x, (size_t)(t0 + r) * DK + d) : 0.f;
+      if (OUT) Qs[r * KP + d] = r < n ? ld(q, (size_t)(t0 + r) * DK + d) : 0.f;
+    }
+    for (int i = tid; i < C * NV; i += kThreads) {
+      const int r = i / NV, d = i % NV;
+      Zs[r * VP + d] = r < n ? ld(z, (size_t)(t0 + r) * Dv + d) : 0.f;
+    }
+    if (tid < 32) {
+      const float g = chunk_decays(alpha ? alpha + t0 : nullptr, n, into, out, OUT ? Ds : nullptr);
+      if (tid == 0) gam = g;
+    }
+#pragma unroll
+    for (int xx = 0; xx < RK; ++xx)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        if (OUT) Ss[(r0 + 16 * xx) * VP + c0 + 16 * y] = s[xx][y];
+        if (states) states[(bh * nch + c) * sblk + (size_t)(r0 + 16 * xx) * Dv + j0 + c0 + 16 * y] = s[xx][y];
+      }
+    __syncthreads();
+    if (OUT) {
+      float a[2][2] = {};
+      product<2, 2>(DK, Qs, KP, 1, Xs, 1, KP, a);
+#pragma unroll
+      for (int xx = 0; xx < 2; ++xx)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int i = r0 + 16 * xx, j = c0 + 16 * y;
+          Ps[i * CP + j] = j <= i ? a[xx][y] * Ds[i * CP + j] : 0.f;
+        }
+      float qs[2][2] = {};
+      product<2, 2>(DK, Qs, KP, 1, Ss, VP, 1, qs);
+      __syncthreads();
+#pragma unroll
+      for (int xx = 0; xx < 2; ++xx)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) qs[xx][y] *= into[r0 + 16 * xx];
+      product<2, 2>(C, Ps, CP, 1, Zs, VP, 1, qs);
+#pragma unroll
+      for (int xx = 0; xx < 2; ++xx)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          if (r0 + 16 * xx < n) st(o, (size_t)(t0 + r0 + 16 * xx) * Dv + c0 + 16 * y, qs[xx][y]);
+      __syncthreads();  // P V has read Zs
+    }
+    for (int i = tid; i < C * NV; i += kThreads) {
+      const int r = i / NV;
+      Zs[r * VP + i % NV] *= REV ? into[r] : out[r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int xx = 0; xx < RK; ++xx)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) s[xx][y] *= gam;
+    product<RK, 2>(C, Xs, 1, KP, Zs, VP, 1, s);
+  }
+  if (S_end) {
+#pragma unroll
+    for (int xx = 0; xx < RK; ++xx)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) S_end[bh * sblk + (size_t)(r0 + 16 * xx) * Dv + j0 + c0 + 16 * y] = s[xx][y];
+  }
+}
+
+template <int DK, bool OUT>
+constexpr size_t scan_smem() {
+  return sizeof(float) * (C * (DK + 1) + C * (NV + 1) + (OUT ? DK * (NV + 1) + C * (DK + 1) + 2 * C * CP : 0));
+}
+
+// --------------------------------------------------------------- gradient --
+// One CTA per (b, h, chunk): S the state entering the chunk, R the derivative
+// by the state leaving it.
+template <typename TI, int DK, int DV>
+__global__ void __launch_bounds__(kThreads) gated_simt_grad_kernel(const GatedProblem p, const float* Sst,
+                                                                   const float* Rst) {
+  constexpr int KP = DK + 1, VP = DV + 1, RK = DK / 16, RV = DV / 16;
+  __shared__ float into[C], out[C], gam, row[C], col[C], rr[C], ee[C], through[kThreads / 32];
+  extern __shared__ float sm[];
+  float* Qs = sm;
+  float* Ks = Qs + C * KP;
+  float* Vs = Ks + C * KP;
+  float* Os = Vs + C * VP;
+  float* As = Os + C * VP;  // C x CP
+  float* Bs = As + C * CP;
+  float* Ds = Bs + C * CP;  // D, then M
+  float* Hs = Ds + C * CP;  // DK x VP: S, then R
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r0 = tid >> 4, c0 = tid & 15;
+  const int T = p.T, nch = (T + C - 1) / C;
+  const size_t bh = blockIdx.x / nch;
+  const int c = (int)(blockIdx.x % nch), t0 = c * C, n = min(C, T - t0);
+  const size_t kbase = (bh * T + t0) * DK, vbase = (bh * T + t0) * DV, sbase = (size_t)blockIdx.x * DK * DV;
+  const TI* q = static_cast<const TI*>(p.q) + kbase;
+  const TI* k = static_cast<const TI*>(p.k) + kbase;
+  const TI* v = static_cast<const TI*>(p.v) + vbase;
+  const TI* dO = static_cast<const TI*>(p.dO) + vbase;
+  for (int i = tid; i < C * DK; i += kThreads) {
+    const int r = i / DK, d = i % DK;
+    Qs[r * KP + d] = r < n ? ld(q, i) : 0.f;
+    Ks[r * KP + d] = r < n ? ld(k, i) : 0.f;
+  }
+  for (int i = tid; i < C * DV; i += kThreads) {
+    const int r = i / DV, d = i % DV;
+    Vs[r * VP + d] = r < n ? ld(v, i) : 0.f;
+    Os[r * VP + d] = r < n ? ld(dO, i) : 0.f;
+  }
+  for (int i = tid; i < DK * DV; i += kThreads) Hs[(i / DV) * VP + i % DV] = Sst[sbase + i];
+  if (tid < 32) {
+    const float g = chunk_decays(p.alpha ? p.alpha + bh * T + t0 : nullptr, n, into, out, Ds);
+    if (tid == 0) gam = g;
+  }
+  __syncthreads();
+  {
+    float a[2][2] = {}, b[2][2] = {};
+    product<2, 2>(DK, Qs, KP, 1, Ks, 1, KP, a);
+    product<2, 2>(DV, Os, VP, 1, Vs, 1, VP, b);
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int i = r0 + 16 * x, j = c0 + 16 * y, at = i * CP + j;
+        const float d = Ds[at];
+        As[at] = j <= i ? a[x][y] * d : 0.f;
+        Bs[at] = j <= i ? b[x][y] * d : 0.f;
+        Ds[at] = j < i ? a[x][y] * b[x][y] * d : 0.f;
+      }
+  }
+  __syncthreads();
+  if (tid < C) {  // row and column sums of M
+    float x = 0.f, y = 0.f;
+#pragma unroll 8
+    for (int j = 0; j < C; ++j) {
+      x += Ds[tid * CP + j];
+      y += Ds[j * CP + tid];
+    }
+    row[tid] = x;
+    col[tid] = y;
+  }
+  // rows r0 + 16 x of a C x (16 RY) result, inter-chunk part `in` scaled by its row's decay
+  auto rowdot16 = [&](float x) {  // over the 16 threads of a row
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+  };
+  {
+    float in[2][RK] = {};
+    product<2, RK>(DV, Os, VP, 1, Hs, 1, VP, in);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int i = r0 + 16 * x;
+      float dot = 0.f;
+#pragma unroll
+      for (int y = 0; y < RK; ++y) {
+        in[x][y] *= into[i];
+        dot = fmaf(in[x][y], Qs[i * KP + c0 + 16 * y], dot);
+      }
+      dot = rowdot16(dot);
+      if (c0 == 0) rr[i] = dot;
+    }
+    product<2, RK>(C, Bs, CP, 1, Ks, KP, 1, in);
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int y = 0; y < RK; ++y)
+        if (r0 + 16 * x < n)
+          st(static_cast<TI*>(p.dq) + kbase, (size_t)(r0 + 16 * x) * DK + c0 + 16 * y, in[x][y]);
+  }
+  __syncthreads();
+  {
+    float sr = 0.f;  // <S, R>, while R takes the place of S
+    for (int i = tid; i < DK * DV; i += kThreads) {
+      const float x = Rst[sbase + i];
+      float* h = Hs + (i / DV) * VP + i % DV;
+      sr = fmaf(*h, x, sr);
+      *h = x;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sr += __shfl_xor_sync(0xffffffffu, sr, o);
+    if (lane == 0) through[warp] = sr;
+  }
+  __syncthreads();
+  {
+    float in[2][RK] = {};
+    product<2, RK>(DV, Vs, VP, 1, Hs, 1, VP, in);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int j = r0 + 16 * x;
+      float dot = 0.f;
+#pragma unroll
+      for (int y = 0; y < RK; ++y) {
+        in[x][y] *= out[j];
+        dot = fmaf(in[x][y], Ks[j * KP + c0 + 16 * y], dot);
+      }
+      dot = rowdot16(dot);
+      if (c0 == 0) ee[j] = dot;
+    }
+    product<2, RK>(C, Bs, 1, CP, Qs, KP, 1, in);
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int y = 0; y < RK; ++y)
+        if (r0 + 16 * x < n)
+          st(static_cast<TI*>(p.dk) + kbase, (size_t)(r0 + 16 * x) * DK + c0 + 16 * y, in[x][y]);
+  }
+  {
+    float in[2][RV] = {};
+    product<2, RV>(DK, Ks, KP, 1, Hs, VP, 1, in);
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int y = 0; y < RV; ++y) in[x][y] *= out[r0 + 16 * x];
+    product<2, RV>(C, As, 1, CP, Os, VP, 1, in);
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int y = 0; y < RV; ++y)
+        if (r0 + 16 * x < n)
+          st(static_cast<TI*>(p.dv) + vbase, (size_t)(r0 + 16 * x) * DV + c0 + 16 * y, in[x][y]);
+  }
+  if (!p.dlog_alpha) return;
+  __syncthreads();
+  if (warp == 0) {
+    float sr = 0.f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) sr += through[w];
+    float suf = row[lane] - col[lane] + rr[lane], pre = ee[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float x = __shfl_down_sync(0xffffffffu, suf, o), y = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane + o < 32) suf += x;
+      if (lane >= o) pre += y;
+    }
+    pre = __shfl_up_sync(0xffffffffu, pre, 1);  // writes before this token
+    if (lane == 0) pre = 0.f;
+    // no path crosses a wipe: its derivative is 0, not the sums' rounding
+    if (lane < n)
+      p.dlog_alpha[bh * T + t0 + lane] = p.alpha[bh * T + t0 + lane] == 0.f ? 0.f : suf + pre + gam * sr;
+  }
+}
+
+template <int DK, int DV>
+constexpr size_t grad_smem() {
+  return sizeof(float) * (2 * C * (DK + 1) + 2 * C * (DV + 1) + 3 * C * CP + DK * (DV + 1));
+}
+
+template <typename TI, int DK, bool REV, bool OUT>
+cudaError_t scan(const GatedProblem& p, float* states, cudaStream_t stream) {
+  auto kern = gated_simt_scan_kernel<TI, DK, REV, OUT>;
+  constexpr size_t smem = scan_smem<DK, OUT>();
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)((size_t)p.B * p.H * (p.Dv / NV)), kThreads, smem, stream>>>(p, states);
+  return cudaGetLastError();
+}
+
+template <typename TI, int DK, int DV>
+cudaError_t grad(const GatedProblem& p, const float* S, const float* R, cudaStream_t stream) {
+  auto kern = gated_simt_grad_kernel<TI, DK, DV>;
+  constexpr size_t smem = grad_smem<DK, DV>();
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)((size_t)p.B * p.H * ((p.T + C - 1) / C)), kThreads, smem, stream>>>(p, S, R);
+  return cudaGetLastError();
+}
+
+template <typename TI>
+cudaError_t bwd(const GatedProblem& p, cudaStream_t stream) {
+  const size_t n = (size_t)p.B * p.H * ((p.T + C - 1) / C) * p.Dk * p.Dv;
+  float* S = static_cast<float*>(p.scratch);
+  float* R = S + n;
+  cudaError_t e = p.Dk == 128 ? scan<TI, 128, false, false>(p, S, stream) : scan<TI, 64, false, false>(p, S, stream);
+  if (e == cudaSuccess)
+    e = p.Dk == 128 ? scan<TI, 128, true, false>(p, R, stream) : scan<TI, 64, true, false>(p, R, stream);
+  if (e != cudaSuccess) return e;
+  if (p.Dk == 128) return p.Dv == 128 ? grad<TI, 128, 128>(p, S, R, stream) : grad<TI, 128, 64>(p, S, R, stream);
+  return p.Dv == 128 ? grad<TI, 64, 128>(p, S, R, stream) : grad<TI, 64, 64>(p, S, R, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_gated_simt_fwd(const GatedProblem& p, cudaStream_t stream) {
+  if (p.bf16)
+    return p.Dk == 128 ? scan<__nv_bfloat16, 128, false, true>(p, nullptr, stream)
+                       : scan<__nv_bfloat16, 64, false, true>(p, nullptr, stream);
+  return p.Dk == 128 ? scan<float, 128, false, true>(p, nullptr, stream)
+                     : scan<float, 64, false, true>(p, nullptr, stream);
+}
+
+cudaError_t launch_gated_simt_bwd(const GatedProblem& p, cudaStream_t stream) {
+  return p.bf16 ? bwd<__nv_bfloat16>(p, stream) : bwd<float>(p, stream);
+}
+
+}  // namespace dn

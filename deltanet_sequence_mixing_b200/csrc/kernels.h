@@ -132,6 +132,71 @@ struct BwdProblem {
 size_t chunk_bwd_state_bytes(int B, int H, int T, int Dk, int Dv);
 cudaError_t launch_chunk_bwd(const BwdProblem& p, cudaStream_t st);
 
+// Gated linear recurrence S_t = alpha_t S_{t-1} + k_t^T v_t, o_t = q_t S_t.
+struct GatedProblem {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* alpha;  // (B,H,T), nullable (1)
+  const float* S0;     // nullable (0)
+  void* o;             // forward
+  float* S_out;        // forward, nullable
+  const void* dO;      // gradient: element type of q
+  const float* dS_T;   // gradient, nullable (0)
+  void* dq;            // gradient: element type of q
+  void* dk;
+  void* dv;
+  float* dlog_alpha;   // gradient, null when alpha is null
+  float* dS0;          // gradient, nullable
+  void* scratch;       // workspace behind the status word
+  int B, H, T, Dk, Dv;
+  int bf16;
+  unsigned int* status;
+};
+// Tokens of a chunk of the CUDA-core kernels (the float32 path).
+constexpr int kGatedSimtChunk = 32;
+cudaError_t launch_gated_simt_fwd(const GatedProblem& p, cudaStream_t stream);
+cudaError_t launch_gated_simt_bwd(const GatedProblem& p, cudaStream_t stream);
+
+// One token of it for every cached state, in place.
+struct GatedStepProblem {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* alpha;  // (B,H), nullable
+  float* S;
+  void* o;
+  int B, H, Dk, Dv;
+  int bf16;
+};
+cudaError_t launch_gated_step(const GatedStepProblem& p, cudaStream_t st);
+
+// Per-head norm and rotation of queries and keys.
+struct QkProblem {
+  const void* q;           // (B,T,Hq,D) by strides, in elements
+  const void* k;           // (B,T,Hk,D)
+  const float* q_weight;   // (D), nullable (1)
+  const float* k_weight;
+  const long long* positions;  // (B,T) with row stride pos_stride_b, nullable (t)
+  const float* inv_freq;   // (rot / 2)
+  void* q_out;             // forward: (B,Hq,T,D); gradient: dL/dq by dqs_*
+  void* k_out;
+  const void* dq_in;       // gradient: (B,Hq,T,D)
+  const void* dk_in;
+  float* dq_weight;        // gradient, nullable
+  float* dk_weight;
+  float* partial;          // gradient: workspace, qk_bwd_ctas x 2 x D (null: no weight gradient)
+  int B, T, Hq, Hk, D, rot;
+  long long qs_b, qs_t, qs_h, ks_b, ks_t, ks_h, pos_stride_b;
+  long long dqs_b, dqs_t, dqs_h, dks_b, dks_t, dks_h;
+  float eps;
+  int l2, silu, interleaved, bf16, grad_bf16;
+};
+// CTAs (rows of partial weight sums) of the gradient.
+int qk_bwd_ctas(int B, int T, int Hq, int Hk);
+cudaError_t launch_qk_fwd(const QkProblem& p, cudaStream_t st);
+cudaError_t launch_qk_bwd(const QkProblem& p, cudaStream_t st);
+
 // Bounded-wait self test.
 cudaError_t launch_wait_selftest(unsigned int* status, long long wait_ns, cudaStream_t st);
 

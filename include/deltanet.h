@@ -292,6 +292,131 @@ int deltanet_chunk_bwd(const void *q, const void *k, const void *v,
                        void *workspace, size_t ws_bytes, void *cuda_stream);
 
 /*
+ * Gated linear recurrence: the additive state of [P3] "Linear attention"
+ * without feature map and normaliser, with the decay of [P1]'s forgetting line
+ * (cache = alpha S_old + S_new):
+ *     S_t = alpha_t S_{t-1} + k_t^T v_t        (alpha_t = 1 when alpha == NULL)
+ *     o_t = q_t S_t                            (state after the write)
+ * evaluated in chunks whose decays are products of alpha over the tokens
+ * between a write and a read; long sequences over few heads are cut into
+ * segments that run side by side, joined through their states in float32.
+ *
+ *   q, k       (B,H,T,Dk), v (B,H,T,Dv), element type dt, 16-byte aligned.
+ *   alpha      (B,H,T) float32 in [0,1], or NULL.  0 forgets everything before
+ *              the token exactly (packed documents); a token with k = 0 and
+ *              alpha = 1 leaves the state as it is (padding).
+ *   S0         (B,H,Dk,Dv) float32, or NULL for zero.
+ *   o          (B,H,T,Dv), element type dt, 16-byte aligned.
+ *   S_out      (B,H,Dk,Dv) float32, or NULL.  May equal S0.
+ *   Dk, Dv     64 or 128.   T >= 0, any length; T == 0 copies S0 (or zeros) to
+ *              S_out, and the token buffers may then be NULL.
+ *   workspace  gated_linear_attn_workspace_bytes(...) bytes, 16-byte aligned,
+ *              cleared once with deltanet_workspace_init (the status word);
+ *              calls that overlap on the GPU need one each.
+ * The sizes depend on the current device's SM count, which must be that of the
+ * call.  Arithmetic: bf16 inputs run on tensor cores with float32 accumulation
+ * and state (products with rounded operands: the decayed scores and the state
+ * that o reads; the state itself carries about 17 bits more than bf16);
+ * float32 inputs run in float32.  The result is deterministic.  A NaN or Inf
+ * in q, k or v reaches, beside what the recurrence itself spreads it to, the
+ * other tokens of its chunk (at most 128 tokens) of the same (b, h).
+ */
+size_t gated_linear_attn_workspace_bytes(int B, int H, int T, int Dk, int Dv, dn_dtype dt);
+int gated_linear_attn_fwd(const void *q, const void *k, const void *v,
+                          const float *alpha, const float *S0, void *o, float *S_out,
+                          int B, int H, int T, int Dk, int Dv, dn_dtype dt,
+                          void *workspace, size_t ws_bytes, void *cuda_stream);
+
+/*
+ * Gradient of gated_linear_attn_fwd for L = sum(dO * o) + sum(dS_T * S_T).
+ * Unlike deltanet_chunk_bwd, dq (B,H,T,Dk), dk (B,H,T,Dk) and dv (B,H,T,Dv)
+ * have the element type dt, 16-byte aligned: they are summed in float32 and
+ * rounded once, to what the projections' own gradients read.
+ *     dlog_alpha (B,H,T) float32 = alpha * dL/dalpha (nullable; NULL when
+ *                alpha is NULL);   dS0 (B,H,Dk,Dv) float32 (nullable).
+ * dO has the shape and element type of o; dS_T is (B,H,Dk,Dv) float32 or NULL.
+ * Outputs overlap neither inputs nor each other.  The workspace is
+ * gated_linear_attn_bwd_workspace_bytes(...) bytes, otherwise as above.
+ * T == 0 copies dS_T (or zeros) to dS0.  The result is deterministic.
+ */
+size_t gated_linear_attn_bwd_workspace_bytes(int B, int H, int T, int Dk, int Dv, dn_dtype dt);
+int gated_linear_attn_bwd(const void *q, const void *k, const void *v,
+                          const float *alpha, const float *S0, const void *dO, const float *dS_T,
+                          void *dq, void *dk, void *dv, float *dlog_alpha, float *dS0,
+                          int B, int H, int T, int Dk, int Dv, dn_dtype dt,
+                          void *workspace, size_t ws_bytes, void *cuda_stream);
+
+/*
+ * One token of the gated linear recurrence for B x H cached states, in place:
+ * S <- alpha S + k^T v, o = q S.  Layouts and rules of deltanet_decode_step,
+ * without beta; each state is read once and written once.
+ */
+int gated_linear_attn_decode_step(const void *q, const void *k, const void *v,
+                                  const float *alpha, float *S, void *o,
+                                  int B, int H, int Dk, int Dv, dn_dtype dt, void *cuda_stream);
+
+/*
+ * Per-head norm of queries and keys with the rotation by position, in one
+ * pass: what the layer does between its projection and a mixing call above.
+ * q and k are read by strides from (B,T,H,D) views (a fused projection's
+ * output, say) and written as the contiguous (B,H,T,D) those calls take.
+ * Per row x of D values:
+ *     z = x, or silu(x) with DN_QK_SILU
+ *     y = w * z / sqrt(mean(z^2) + eps), or with DN_QK_L2 w * z / max(||z||_2, eps)
+ *     the first `rot` columns of y turned in pairs by position * inv_freq[i]:
+ *     columns (i, i + rot/2), or with DN_QK_INTERLEAVED (2i, 2i + 1);
+ *     (a, b) -> (a cos - b sin, b cos + a sin); the other columns pass.
+ * (DN_QK_SILU | DN_QK_L2, eps = 1e-12, rot = 0 and no weights is the map of
+ * DN_OPT_PRESTEP.)
+ *
+ *   q_weight, k_weight  (D) float32, or NULL for 1.
+ *   positions   int64, element (b, t) at b * pos_stride_b + t (pos_stride_b = 0:
+ *               one row for every b), or NULL for t.  Any value: the angle is
+ *               formed in float64.
+ *   inv_freq    (rot / 2) float32; unused (may be NULL) when rot == 0.
+ *   q_out, k_out  (B,Hq,T,D), (B,Hk,T,D), element type dt.
+ *   D 64 or 128; rot a multiple of 16, 0 <= rot <= D; Hq, Hk >= 0 (0: that
+ *   tensor's pointers may be NULL); T >= 0.
+ *   qs_*, ks_*  strides of q and k in elements over b, t and h; rows are
+ *               contiguous.  Bases and strides are multiples of 16 bytes
+ *               (DN_ERR_ALIGNMENT otherwise); strides are not negative.
+ *   eps         > 0 and finite.
+ * Squares are summed in float32.  An output may not overlap an input or the
+ * other output.
+ */
+enum { DN_QK_L2 = 1, DN_QK_SILU = 2, DN_QK_INTERLEAVED = 4 };
+int qk_norm_rope_fwd(const void *q, const void *k, const float *q_weight, const float *k_weight,
+                     const long long *positions, const float *inv_freq, void *q_out, void *k_out,
+                     int B, int T, int Hq, int Hk, int D, int rot,
+                     long long qs_b, long long qs_t, long long qs_h,
+                     long long ks_b, long long ks_t, long long ks_h, long long pos_stride_b,
+                     float eps, unsigned int options, dn_dtype dt, void *cuda_stream);
+
+/*
+ * Gradient of qk_norm_rope_fwd.  dq_out (B,Hq,T,D) and dk_out (B,Hk,T,D) are
+ * the derivatives by its outputs, of element type grad_dt: dt, or float32 (what
+ * deltanet_chunk_bwd writes).  dq and dk take the derivatives by q and k, of
+ * element type dt, by strides of their own (a fused gradient's slices, say;
+ * rows that overlap one another are rejected).  dq_weight, dk_weight: (D)
+ * float32, NULL where not wanted or where the weight is NULL; summed over all
+ * rows in a fixed order (deterministic).  workspace:
+ * qk_norm_rope_bwd_workspace_bytes(...) bytes, 16-byte aligned, needs no
+ * clearing; may be NULL when neither weight's derivative is asked for.
+ */
+size_t qk_norm_rope_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int D);
+int qk_norm_rope_bwd(const void *q, const void *k, const void *dq_out, const void *dk_out,
+                     const float *q_weight, const float *k_weight,
+                     const long long *positions, const float *inv_freq,
+                     void *dq, void *dk, float *dq_weight, float *dk_weight,
+                     int B, int T, int Hq, int Hk, int D, int rot,
+                     long long qs_b, long long qs_t, long long qs_h,
+                     long long ks_b, long long ks_t, long long ks_h,
+                     long long dqs_b, long long dqs_t, long long dqs_h,
+                     long long dks_b, long long dks_t, long long dks_h, long long pos_stride_b,
+                     float eps, unsigned int options, dn_dtype dt, dn_dtype grad_dt,
+                     void *workspace, size_t ws_bytes, void *cuda_stream);
+
+/*
  * Synchronise `cuda_stream` and read the sticky device status word of
  * `workspace`: DN_OK, or DN_ERR_DEVICE_TIMEOUT if any earlier kernel given
  * this workspace ran out of a bounded wait (results of that call are then
