@@ -360,6 +360,11 @@ int validate_gated_sizes(int B, int H, int T, int Dk, int Dv, int dt) {
   return DN_OK;
 }
 
+// The segments of a bf16 call on the current device.
+void gated_split(int B, int H, int T, int Dv, int* G, int* seg_chunks) {
+  dn::gated_segments(B * H, T, Dv, sm_count_now(), G, seg_chunks);
+}
+
 // The state of the sequence's end when there are no tokens.
 int carry_state(float* dst, const float* src, size_t bytes, cudaStream_t st) {
   if (!dst || dst == src || bytes == 0) return DN_OK;
@@ -439,7 +444,10 @@ extern "C" {
 
 size_t gated_linear_attn_workspace_bytes(int B, int H, int T, int Dk, int Dv, dn_dtype dt) {
   if (validate_gated_sizes(B, H, T, Dk, Dv, dt) != DN_OK) return 0;
-  return kStatusBytes;
+  if (dt == DN_F32 || (long long)B * H == 0 || T == 0) return kStatusBytes;
+  int G, per;
+  gated_split(B, H, T, Dv, &G, &per);
+  return kStatusBytes + dn::gated_segment_bytes(B * H, G, Dk, Dv);
 }
 
 int gated_linear_attn_fwd(const void* q, const void* k, const void* v, const float* alpha, const float* S0, void* o,
@@ -469,7 +477,9 @@ int gated_linear_attn_fwd(const void* q, const void* k, const void* v, const flo
   p.bf16 = dt == DN_BF16;
   p.status = static_cast<unsigned int*>(workspace);
   p.scratch = static_cast<uint8_t*>(workspace) + kStatusBytes;
-  return map_cuda(dn::launch_gated_simt_fwd(p, st));
+  if (!p.bf16) return map_cuda(dn::launch_gated_simt_fwd(p, st));
+  gated_split(B, H, T, Dv, &p.G, &p.seg_chunks);
+  return map_cuda(dn::launch_gated_tc_fwd(p, st));
 }
 
 size_t gated_linear_attn_bwd_workspace_bytes(int B, int H, int T, int Dk, int Dv, dn_dtype dt) {

@@ -67,8 +67,8 @@ struct DecodeProblem {
 cudaError_t launch_decode(const DecodeProblem& p, cudaStream_t st);
 
 // 3-D TMA map over a (BH, T, D) bf16 tensor: 64 x 64 boxes, 128-byte swizzle,
-// rows past T read as zeros.
-bool make_tmap_3d_bf16(CUtensorMap* m, const void* base, int D, int T, int BH);
+// rows past T read as zeros; `rows`: rows of a box (at most 256).
+bool make_tmap_3d_bf16(CUtensorMap* m, const void* base, int D, int T, int BH, int rows = 64);
 
 // Per-chunk WY factors written by the pre-pass and read by the chunk kernels
 // (C = 64 or 128 token chunks).
@@ -152,9 +152,27 @@ struct GatedProblem {
   int B, H, T, Dk, Dv;
   int bf16;
   unsigned int* status;
+  int G, seg_chunks;   // bf16: segments of the sequence and their chunks (gated_segments)
 };
 // Tokens of a chunk of the CUDA-core kernels (the float32 path).
 constexpr int kGatedSimtChunk = 32;
+// Tokens of a chunk of the tensor-core kernels (the bf16 path).
+constexpr int kGatedChunk = 128;
+// What the tensor-core scan kernels take beside their tensor maps.
+struct GatedScan {
+  const float* alpha;
+  const float* S_in;      // state entering the sequence (in the scan's direction), nullable
+  size_t S_in_stride;     // floats from one (b, h) to the next
+  float* S_out;           // state leaving it, nullable
+  float* seg_decay;       // [BH][G] product of alpha over a segment
+  float* seg_end;         // [BH][G][Dk][Dv] a segment's end state from zero
+  unsigned int* status;
+  int T, Dv, G, seg_chunks;
+};
+// The split of T into G segments of seg_chunks chunks (the last may be shorter).
+void gated_segments(int BH, int T, int Dv, int sms, int* G, int* seg_chunks);
+size_t gated_segment_bytes(int BH, int G, int Dk, int Dv);
+cudaError_t launch_gated_tc_fwd(const GatedProblem& p, cudaStream_t st);
 cudaError_t launch_gated_simt_fwd(const GatedProblem& p, cudaStream_t stream);
 cudaError_t launch_gated_simt_bwd(const GatedProblem& p, cudaStream_t stream);
 

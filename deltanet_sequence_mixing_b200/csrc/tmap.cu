@@ -29,12 +29,12 @@ EncodeTiledFn encode_fn() {
 
 }  // namespace
 
-bool make_tmap_3d_bf16(CUtensorMap* m, const void* base, int D, int T, int BH) {
+bool make_tmap_3d_bf16(CUtensorMap* m, const void* base, int D, int T, int BH, int rows) {
   EncodeTiledFn enc = encode_fn();
-  if (!enc || !base || D % 64 != 0 || T < 1 || BH < 1) return false;
+  if (!enc || !base || D % 64 != 0 || T < 1 || BH < 1 || rows < 1 || rows > 256) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)T, (cuuint64_t)BH};
   const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)T * D * 2};
-  const cuuint32_t box[3] = {64, 64, 1};
+  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
