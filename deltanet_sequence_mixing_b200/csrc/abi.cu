@@ -484,6 +484,12 @@ int gated_linear_attn_fwd(const void* q, const void* k, const void* v, const flo
 
 size_t gated_linear_attn_bwd_workspace_bytes(int B, int H, int T, int Dk, int Dv, dn_dtype dt) {
   if (validate_gated_sizes(B, H, T, Dk, Dv, dt) != DN_OK) return 0;
+  if ((long long)B * H == 0 || T == 0) return kStatusBytes;
+  if (dt == DN_BF16) {
+    int G, per;
+    gated_split(B, H, T, Dv, &G, &per);
+    return kStatusBytes + dn::gated_bwd_bytes(B * H, T, G, Dk, Dv);
+  }
   const size_t chunks = ((size_t)T + dn::kGatedSimtChunk - 1) / dn::kGatedSimtChunk;
   return kStatusBytes + 2 * (size_t)B * H * chunks * Dk * Dv * 4;
 }
@@ -526,7 +532,9 @@ int gated_linear_attn_bwd(const void* q, const void* k, const void* v, const flo
   p.bf16 = dt == DN_BF16;
   p.status = static_cast<unsigned int*>(workspace);
   p.scratch = static_cast<uint8_t*>(workspace) + kStatusBytes;
-  return map_cuda(dn::launch_gated_simt_bwd(p, st));
+  if (!p.bf16) return map_cuda(dn::launch_gated_simt_bwd(p, st));
+  gated_split(B, H, T, Dv, &p.G, &p.seg_chunks);
+  return map_cuda(dn::launch_gated_tc_bwd(p, st));
 }
 
 int gated_linear_attn_decode_step(const void* q, const void* k, const void* v, const float* alpha, float* S, void* o,

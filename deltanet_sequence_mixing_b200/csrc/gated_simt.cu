@@ -1,4 +1,4 @@
-// Gated linear recurrence on CUDA cores (float32 arithmetic): forward and
+// Gated linear recurrence on float32 inputs, on CUDA cores: forward and
 // gradient.  Per (b, h), with a Dk x Dv state,
 //     S_t = alpha_t S_{t-1} + k_t^T v_t,   o_t = q_t S_t.
 //
@@ -25,8 +25,6 @@
 // of (k, v); one CTA per (b, h, 32 columns of Dv), serial over chunks), which
 // stores each chunk's entry state when the gradient needs it, and the gradient
 // of every chunk side by side.
-#include <cuda_bf16.h>
-
 #include "kernels.h"
 
 namespace dn {
@@ -34,17 +32,6 @@ namespace {
 
 constexpr int C = kGatedSimtChunk, kThreads = 256, NV = 32, CP = C + 1;
 static_assert(C == 32, "one lane per token of a chunk");
-
-template <typename TI>
-__device__ __forceinline__ float ld(const TI* p, size_t i);
-template <>
-__device__ __forceinline__ float ld<float>(const float* p, size_t i) { return p[i]; }
-template <>
-__device__ __forceinline__ float ld<__nv_bfloat16>(const __nv_bfloat16* p, size_t i) {
-  return __bfloat162float(p[i]);
-}
-__device__ __forceinline__ void st(float* p, size_t i, float x) { p[i] = x; }
-__device__ __forceinline__ void st(__nv_bfloat16* p, size_t i, float x) { p[i] = __float2bfloat16_rn(x); }
 
 // acc[x][y] += sum_{k < nk} A[(r0 + 16 x) ars + k acs] B[k brs + (c0 + 16 y) bcs]
 // for thread (r0, c0) of the CTA's 16 x 16 grid.
@@ -100,7 +87,7 @@ __device__ __forceinline__ float chunk_decays(const float* alpha, int n, float* 
 // Reverse: x = q, z = dO, chunks from the last, R <- gamma R + Q^T diag(G) dO.
 // `states` (if not null) takes the state that each chunk is entered with, in
 // the scan's own direction.
-template <typename TI, int DK, bool REV, bool OUT>
+template <int DK, bool REV, bool OUT>
 __global__ void __launch_bounds__(kThreads) gated_simt_scan_kernel(const GatedProblem p, float* states) {
   constexpr int KP = DK + 1, VP = NV + 1, RK = DK / 16;
   __shared__ float into[C], out[C], gam;
@@ -116,10 +103,10 @@ __global__ void __launch_bounds__(kThreads) gated_simt_scan_kernel(const GatedPr
   const size_t bh = blockIdx.x / nsl;
   const int j0 = (int)(blockIdx.x % nsl) * NV;
   const size_t sblk = (size_t)DK * Dv;
-  const TI* x = static_cast<const TI*>(REV ? p.q : p.k) + bh * T * DK;
-  const TI* q = static_cast<const TI*>(p.q) + bh * T * DK;
-  const TI* z = static_cast<const TI*>(REV ? p.dO : p.v) + bh * T * Dv + j0;
-  TI* o = OUT ? static_cast<TI*>(p.o) + bh * T * Dv + j0 : nullptr;
+  const float* x = static_cast<const float*>(REV ? p.q : p.k) + bh * T * DK;
+  const float* q = static_cast<const float*>(p.q) + bh * T * DK;
+  const float* z = static_cast<const float*>(REV ? p.dO : p.v) + bh * T * Dv + j0;
+  float* o = OUT ? static_cast<float*>(p.o) + bh * T * Dv + j0 : nullptr;
   const float* alpha = p.alpha ? p.alpha + bh * T : nullptr;
   const float* S_in = REV ? p.dS_T : p.S0;
   float* S_end = REV ? p.dS0 : p.S_out;
@@ -136,12 +123,12 @@ __global__ void __launch_bounds__(kThreads) gated_simt_scan_kernel(const GatedPr
     __syncthreads();  // the products of the chunk before have read the tiles
     for (int i = tid; i < C * DK; i += kThreads) {
       const int r = i / DK, d = i % DK;
-      Xs[r * KP + d] = r < n ? ld(x, (size_t)(t0 + r) * DK + d) : 0.f;
-      if (OUT) Qs[r * KP + d] = r < n ? ld(q, (size_t)(t0 + r) * DK + d) : 0.f;
+      Xs[r * KP + d] = r < n ? x[(size_t)(t0 + r) * DK + d] : 0.f;
+      if (OUT) Qs[r * KP + d] = r < n ? q[(size_t)(t0 + r) * DK + d] : 0.f;
     }
     for (int i = tid; i < C * NV; i += kThreads) {
       const int r = i / NV, d = i % NV;
-      Zs[r * VP + d] = r < n ? ld(z, (size_t)(t0 + r) * Dv + d) : 0.f;
+      Zs[r * VP + d] = r < n ? z[(size_t)(t0 + r) * Dv + d] : 0.f;
     }
     if (tid < 32) {
       const float g = chunk_decays(alpha ? alpha + t0 : nullptr, n, into, out, OUT ? Ds : nullptr);
@@ -177,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) gated_simt_scan_kernel(const GatedPr
       for (int xx = 0; xx < 2; ++xx)
 #pragma unroll
         for (int y = 0; y < 2; ++y)
-          if (r0 + 16 * xx < n) st(o, (size_t)(t0 + r0 + 16 * xx) * Dv + c0 + 16 * y, qs[xx][y]);
+          if (r0 + 16 * xx < n) o[(size_t)(t0 + r0 + 16 * xx) * Dv + c0 + 16 * y] = qs[xx][y];
       __syncthreads();  // P V has read Zs
     }
     for (int i = tid; i < C * NV; i += kThreads) {
@@ -207,7 +194,7 @@ constexpr size_t scan_smem() {
 // --------------------------------------------------------------- gradient --
 // One CTA per (b, h, chunk): S the state entering the chunk, R the derivative
 // by the state leaving it.
-template <typename TI, int DK, int DV>
+template <int DK, int DV>
 __global__ void __launch_bounds__(kThreads) gated_simt_grad_kernel(const GatedProblem p, const float* Sst,
                                                                    const float* Rst) {
   constexpr int KP = DK + 1, VP = DV + 1, RK = DK / 16, RV = DV / 16;
@@ -226,19 +213,19 @@ __global__ void __launch_bounds__(kThreads) gated_simt_grad_kernel(const GatedPr
   const size_t bh = blockIdx.x / nch;
   const int c = (int)(blockIdx.x % nch), t0 = c * C, n = min(C, T - t0);
   const size_t kbase = (bh * T + t0) * DK, vbase = (bh * T + t0) * DV, sbase = (size_t)blockIdx.x * DK * DV;
-  const TI* q = static_cast<const TI*>(p.q) + kbase;
-  const TI* k = static_cast<const TI*>(p.k) + kbase;
-  const TI* v = static_cast<const TI*>(p.v) + vbase;
-  const TI* dO = static_cast<const TI*>(p.dO) + vbase;
+  const float* q = static_cast<const float*>(p.q) + kbase;
+  const float* k = static_cast<const float*>(p.k) + kbase;
+  const float* v = static_cast<const float*>(p.v) + vbase;
+  const float* dO = static_cast<const float*>(p.dO) + vbase;
   for (int i = tid; i < C * DK; i += kThreads) {
     const int r = i / DK, d = i % DK;
-    Qs[r * KP + d] = r < n ? ld(q, i) : 0.f;
-    Ks[r * KP + d] = r < n ? ld(k, i) : 0.f;
+    Qs[r * KP + d] = r < n ? q[i] : 0.f;
+    Ks[r * KP + d] = r < n ? k[i] : 0.f;
   }
   for (int i = tid; i < C * DV; i += kThreads) {
     const int r = i / DV, d = i % DV;
-    Vs[r * VP + d] = r < n ? ld(v, i) : 0.f;
-    Os[r * VP + d] = r < n ? ld(dO, i) : 0.f;
+    Vs[r * VP + d] = r < n ? v[i] : 0.f;
+    Os[r * VP + d] = r < n ? dO[i] : 0.f;
   }
   for (int i = tid; i < DK * DV; i += kThreads) Hs[(i / DV) * VP + i % DV] = Sst[sbase + i];
   if (tid < 32) {
@@ -299,7 +286,7 @@ __global__ void __launch_bounds__(kThreads) gated_simt_grad_kernel(const GatedPr
 #pragma unroll
       for (int y = 0; y < RK; ++y)
         if (r0 + 16 * x < n)
-          st(static_cast<TI*>(p.dq) + kbase, (size_t)(r0 + 16 * x) * DK + c0 + 16 * y, in[x][y]);
+          (static_cast<float*>(p.dq) + kbase)[(size_t)(r0 + 16 * x) * DK + c0 + 16 * y] = in[x][y];
   }
   __syncthreads();
   {
@@ -336,7 +323,7 @@ __global__ void __launch_bounds__(kThreads) gated_simt_grad_kernel(const GatedPr
 #pragma unroll
       for (int y = 0; y < RK; ++y)
         if (r0 + 16 * x < n)
-          st(static_cast<TI*>(p.dk) + kbase, (size_t)(r0 + 16 * x) * DK + c0 + 16 * y, in[x][y]);
+          (static_cast<float*>(p.dk) + kbase)[(size_t)(r0 + 16 * x) * DK + c0 + 16 * y] = in[x][y];
   }
   {
     float in[2][RV] = {};
@@ -351,7 +338,7 @@ __global__ void __launch_bounds__(kThreads) gated_simt_grad_kernel(const GatedPr
 #pragma unroll
       for (int y = 0; y < RV; ++y)
         if (r0 + 16 * x < n)
-          st(static_cast<TI*>(p.dv) + vbase, (size_t)(r0 + 16 * x) * DV + c0 + 16 * y, in[x][y]);
+          (static_cast<float*>(p.dv) + vbase)[(size_t)(r0 + 16 * x) * DV + c0 + 16 * y] = in[x][y];
   }
   if (!p.dlog_alpha) return;
   __syncthreads();
@@ -379,9 +366,9 @@ constexpr size_t grad_smem() {
   return sizeof(float) * (2 * C * (DK + 1) + 2 * C * (DV + 1) + 3 * C * CP + DK * (DV + 1));
 }
 
-template <typename TI, int DK, bool REV, bool OUT>
+template <int DK, bool REV, bool OUT>
 cudaError_t scan(const GatedProblem& p, float* states, cudaStream_t stream) {
-  auto kern = gated_simt_scan_kernel<TI, DK, REV, OUT>;
+  auto kern = gated_simt_scan_kernel<DK, REV, OUT>;
   constexpr size_t smem = scan_smem<DK, OUT>();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -389,9 +376,9 @@ cudaError_t scan(const GatedProblem& p, float* states, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-template <typename TI, int DK, int DV>
+template <int DK, int DV>
 cudaError_t grad(const GatedProblem& p, const float* S, const float* R, cudaStream_t stream) {
-  auto kern = gated_simt_grad_kernel<TI, DK, DV>;
+  auto kern = gated_simt_grad_kernel<DK, DV>;
   constexpr size_t smem = grad_smem<DK, DV>();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -399,31 +386,22 @@ cudaError_t grad(const GatedProblem& p, const float* S, const float* R, cudaStre
   return cudaGetLastError();
 }
 
-template <typename TI>
-cudaError_t bwd(const GatedProblem& p, cudaStream_t stream) {
-  const size_t n = (size_t)p.B * p.H * ((p.T + C - 1) / C) * p.Dk * p.Dv;
-  float* S = static_cast<float*>(p.scratch);
-  float* R = S + n;
-  cudaError_t e = p.Dk == 128 ? scan<TI, 128, false, false>(p, S, stream) : scan<TI, 64, false, false>(p, S, stream);
-  if (e == cudaSuccess)
-    e = p.Dk == 128 ? scan<TI, 128, true, false>(p, R, stream) : scan<TI, 64, true, false>(p, R, stream);
-  if (e != cudaSuccess) return e;
-  if (p.Dk == 128) return p.Dv == 128 ? grad<TI, 128, 128>(p, S, R, stream) : grad<TI, 128, 64>(p, S, R, stream);
-  return p.Dv == 128 ? grad<TI, 64, 128>(p, S, R, stream) : grad<TI, 64, 64>(p, S, R, stream);
-}
-
 }  // namespace
 
 cudaError_t launch_gated_simt_fwd(const GatedProblem& p, cudaStream_t stream) {
-  if (p.bf16)
-    return p.Dk == 128 ? scan<__nv_bfloat16, 128, false, true>(p, nullptr, stream)
-                       : scan<__nv_bfloat16, 64, false, true>(p, nullptr, stream);
-  return p.Dk == 128 ? scan<float, 128, false, true>(p, nullptr, stream)
-                     : scan<float, 64, false, true>(p, nullptr, stream);
+  return p.Dk == 128 ? scan<128, false, true>(p, nullptr, stream) : scan<64, false, true>(p, nullptr, stream);
 }
 
 cudaError_t launch_gated_simt_bwd(const GatedProblem& p, cudaStream_t stream) {
-  return p.bf16 ? bwd<__nv_bfloat16>(p, stream) : bwd<float>(p, stream);
+  const size_t n = (size_t)p.B * p.H * ((p.T + C - 1) / C) * p.Dk * p.Dv;
+  float* S = static_cast<float*>(p.scratch);
+  float* R = S + n;
+  cudaError_t e = p.Dk == 128 ? scan<128, false, false>(p, S, stream) : scan<64, false, false>(p, S, stream);
+  if (e == cudaSuccess)
+    e = p.Dk == 128 ? scan<128, true, false>(p, R, stream) : scan<64, true, false>(p, R, stream);
+  if (e != cudaSuccess) return e;
+  if (p.Dk == 128) return p.Dv == 128 ? grad<128, 128>(p, S, R, stream) : grad<128, 64>(p, S, R, stream);
+  return p.Dv == 128 ? grad<64, 128>(p, S, R, stream) : grad<64, 64>(p, S, R, stream);
 }
 
 }  // namespace dn

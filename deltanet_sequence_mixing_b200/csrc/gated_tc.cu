@@ -757,6 +757,498 @@ __global__ void __launch_bounds__(kStateThreads, 1)
   if (warp == kWarpMma) tmem_dealloc(tmem, 256);
 }
 
+// --------------------------------------------------------- gradient kernel --
+// Every chunk's gradient from its entry state S and the derivative R by the
+// state it leaves (both as bf16 hi and lo):
+//   A = tril(Q K^T) * D,  B = tril(dO V^T) * D
+//   dV = A^T dO + diag(c) K R,  dK = B^T Q + diag(c) V R^T,  dQ = B K + diag(G) dO S^T
+// and, where there is a gate, the derivative by log alpha_t: the sum of all
+// paths from a write before t to a read at or after it,
+//   sum_{i >= t > j} M_ij + sum_{i >= t} r_i + sum_{j < t} e_j + gamma <S, R>
+//   M = (Q K^T) * (dO V^T) * D,  r_i = q_i . G_i (dO S^T)_i,  e_j = k_j . c_j (V R^T)_j
+// (the first term: the suffix sum of row sums less column sums of M below its
+// diagonal, both from the same float32 values).  Its sums do not leave the
+// chunk, so no error travels along T; dO S^T and V R^T take hi and lo so that
+// r and e hold to float32, the outputs themselves to one rounding of A or B.
+//
+// One CTA per (b, h, chunk), everything in shared memory at once except the
+// states, which pass through one tile (R hi, S hi) and through A's (R lo, S
+// lo, once dV has been staged there and stored).  Every barrier is used once.
+//   warp 0 TMA, warp 1 MMA, warps 4-11 epilogues (two warps to 32 rows, each
+//   half of the columns), warps 12-19 <S, R> (R in registers) and the sums
+constexpr int kGradThreads = 20 * 32, kGradPlain = 12 * 32, kBarE = 1, kBarT = 2;
+enum : uint32_t {  // single-use mbarriers
+  G_QK = 0, G_VO = 8, G_RH = 16, G_RL = 24, G_SH = 32, G_SL = 40, G_SC = 48, G_P = 56, G_DV = 64, G_XR = 72,
+  G_DK = 80, G_DQ = 88, G_ACCFREE = 96, G_PAFREE = 104, G_RHREAD = 112, G_RLREAD = 120, G_DOTS = 128, G_FIN = 136,
+  G_TMEM = 144, G_ABORT = 148
+};
+template <int DK, int DV>
+struct GradLayout {
+  static constexpr int KB = DK / 64, VB = DV / 64;
+  static constexpr uint32_t SBLK = DK * 128, STATE = VB * SBLK;  // one 64-column block, a state tile
+  static constexpr uint32_t Q_OFF = 0, K_OFF = Q_OFF + KB * kBlk, V_OFF = K_OFF + KB * kBlk, O_OFF = V_OFF + VB * kBlk;
+  static constexpr uint32_t PA_OFF = O_OFF + VB * kBlk, PB_OFF = PA_OFF + 2 * kBlk, X_OFF = PB_OFF + 2 * kBlk;
+  static constexpr uint32_t END = X_OFF + STATE;
+  static constexpr uint32_t DK_OFF = KB <= VB ? V_OFF : END;  // dK is staged over V where it fits
+  static constexpr uint32_t SUF_OFF = END + (KB <= VB ? 0 : KB * kBlk);  // suf[128], block products [4]
+  static constexpr uint32_t THR_OFF = SUF_OFF + 132 * 4;                 // <S, R> of 8 warps, gamma
+  static constexpr uint32_t BAR_OFF = (THR_OFF + 9 * 4 + 7) / 8 * 8;
+  static constexpr uint32_t BYTES = BAR_OFF + 152;
+  static constexpr uint32_t ALLOC = BYTES + 1024;
+  // the rows' sums at the end, over dO: F[2][128], e[2][128], column sums [4][128]
+  static constexpr uint32_t FSUM = O_OFF, ESUM = FSUM + 1024, CSUM = ESUM + 1024;
+  static_assert(ALLOC <= 232448, "shared memory budget");
+  static_assert(END % 1024 == 0, "128-byte swizzle atoms stay aligned");
+};
+// TMEM: scores and dO V^T, then dK's two parts | dV's, then dQ's
+constexpr uint32_t TG_A = 0, TG_B = 128, TG_C = 256, TG_D = 384;
+
+// Sums of 16 columns over the warp's rows: lane l < 16 ends with the sum of
+// column fold16_col(l).
+__device__ __forceinline__ float fold16(float (&v)[16]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1, n = 8; o < 16; o <<= 1, n >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float mine = up ? v[i + n] : v[i], theirs = up ? v[i] : v[i + n];
+      v[i] = mine + __shfl_xor_sync(0xffffffffu, theirs, o);
+    }
+  }
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+}
+__device__ __forceinline__ int fold16_col(int l) {
+  return (l & 1) * 8 + ((l >> 1) & 1) * 4 + ((l >> 2) & 1) * 2 + ((l >> 3) & 1);
+}
+
+// out = f * inter + intra for this thread's row and columns [c0, c0 + NC) into
+// the staged tile; returns the dot product of f * inter with the same row of
+// `with` (which may be the staged tile itself).
+template <int NC, bool DOT>
+__device__ __forceinline__ float grad_row(uint32_t inter, uint32_t intra, float f, const uint8_t* with, uint8_t* stage,
+                                          int row, int c0) {
+  float dot = 0.f;
+#pragma unroll
+  for (int c = 0; c < NC; c += 16) {
+    uint32_t x[16], y[16];
+    tmem_ld16(inter + c0 + c, x);
+    tmem_ld16(intra + c0 + c, y);
+    tmem_wait_ld();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int col = c0 + c + 8 * h;
+      const uint32_t at = (uint32_t)(col >> 6) * kBlk + sw128_off(row, (col >> 3) & 7);
+      float u[8], o[8];
+      if (DOT) unpack_bf16x8(*reinterpret_cast<const uint4*>(with + at), u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = f * __uint_as_float(x[8 * h + e]);
+        if (DOT) dot = fmaf(v, u[e], dot);
+        o[e] = v + __uint_as_float(y[8 * h + e]);
+      }
+      st_bf16x8(stage + at, o);
+    }
+  }
+  return dot;
+}
+
+template <int DK, int DV, bool GATED>
+__global__ void __launch_bounds__(kGradThreads, 1)
+    gated_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                      const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmR,
+                      const __grid_constant__ CUtensorMap tmDQ, const __grid_constant__ CUtensorMap tmDK,
+                      const __grid_constant__ CUtensorMap tmDV, const float* alpha_all, float* dlog_alpha, int T,
+                      unsigned int* status) {
+  using L = GradLayout<DK, DV>;
+  constexpr int KB = L::KB, VB = L::VB;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = warp_uniform(smem_u32(sm));
+  const int tid = threadIdx.x, lane = tid & 31, warp = (int)warp_uniform((uint32_t)tid >> 5), w = warp & 3;
+  const int nch = (T + C - 1) / C, bh = blockIdx.x / nch, c = blockIdx.x % nch, t0 = c * C;
+  const uint32_t bar = sb + L::BAR_OFF;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::BAR_OFF + G_TMEM);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::BAR_OFF + G_ABORT);
+  float* suf = reinterpret_cast<float*>(sm + L::SUF_OFF);
+  float* blk = suf + C;
+  float* thr = reinterpret_cast<float*>(sm + L::THR_OFF);
+  const float* alpha = GATED ? alpha_all + (size_t)bh * T : nullptr;
+
+  if (tid == 0) {
+    for (uint32_t b : {G_QK, G_VO, G_RH, G_RL, G_SH, G_SL, G_SC, G_DV, G_XR, G_DK, G_DQ, G_PAFREE, G_FIN})
+      mbar_init(bar + b, 1);
+    for (uint32_t b : {G_P, G_ACCFREE, G_RHREAD, G_RLREAD, G_DOTS}) mbar_init(bar + b, 8);  // one arrival per warp
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = warp_uniform(*tmem_slot);
+  const WaitCtl wc{abort_flag, status, kWaitLimitNs};
+  auto wait = [&](uint32_t b) { return mbar_wait(bar + b, 0, wc); };
+  auto wait_all = [&](uint32_t b) { return __all_sync(0xffffffffu, wait(b)) != 0; };
+  auto arrive = [&](uint32_t b) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar + b);
+  };
+
+  if (warp == kWarpTma) {
+    if (lane == 0) {
+      const int at = (bh * nch + c) * 2;
+      uint32_t got[6];
+      int n = 0;
+      auto expect = [&](uint32_t b, uint32_t bytes) {
+        mbar_expect_tx(bar + b, bytes);
+        got[n++] = b;
+      };
+      auto state = [&](uint32_t b, const CUtensorMap* m, uint32_t to, int z) {
+        expect(b, L::STATE);
+#pragma unroll
+        for (int i = 0; i < VB; ++i) tma_load_3d(sb + to + i * L::SBLK, m, bar + b, 64 * i, 0, z);
+      };
+      expect(G_QK, 2 * KB * kBlk);
+#pragma unroll
+      for (int i = 0; i < KB; ++i) {
+        tma_load_3d(sb + L::Q_OFF + i * kBlk, &tmQ, bar + G_QK, 64 * i, t0, bh);
+        tma_load_3d(sb + L::K_OFF + i * kBlk, &tmK, bar + G_QK, 64 * i, t0, bh);
+      }
+      expect(G_VO, 2 * VB * kBlk);
+#pragma unroll
+      for (int i = 0; i < VB; ++i) {
+        tma_load_3d(sb + L::O_OFF + i * kBlk, &tmO, bar + G_VO, 64 * i, t0, bh);
+        tma_load_3d(sb + L::V_OFF + i * kBlk, &tmV, bar + G_VO, 64 * i, t0, bh);
+      }
+      state(G_RH, &tmR, L::X_OFF, at);
+      if (GATED) {
+        bool ok = wait(G_PAFREE);
+        if (ok) state(G_RL, &tmR, L::PA_OFF, at + 1);
+        ok = ok && wait(G_XR) && wait(G_RHREAD);
+        if (ok) state(G_SH, &tmS, L::X_OFF, at);
+        ok = ok && wait(G_DK) && wait(G_RLREAD);
+        if (ok) state(G_SL, &tmS, L::PA_OFF, at + 1);
+      } else {
+        if (wait(G_XR)) state(G_SH, &tmS, L::X_OFF, at);
+      }
+      int zero = 0;  // never leave with copies in flight
+      const WaitCtl drain{&zero, status, kWaitLimitNs};
+      for (int i = 0; i < n; ++i) (void)mbar_wait(bar + got[i], 0, drain);
+    }
+  } else if (warp == kWarpMma) {
+    // A: K-major tile of 64-column blocks `ab` apart; B: K-major blocks `bb` apart
+    auto kk = [&](uint32_t d, uint32_t a, uint32_t ab, uint32_t b, uint32_t bb, int depth, int N, uint32_t acc) {
+      const uint32_t id = idesc_bf16(128, N, false, false);
+      const uint64_t da = desc_k(sb + a), db = desc_k(sb + b);
+#pragma unroll
+      for (int ks = 0; ks < depth / 16; ++ks)
+        mma_bf16_ss_elect(tmem + d, desc_step(da, (ks >> 2) * ab + (ks & 3) * 32),
+                          desc_step(db, (ks >> 2) * bb + (ks & 3) * 32), id, acc | (uint32_t)(ks > 0));
+    };
+    // A: K-major; B: MN-major tile (rows are the depth), blocks `bb` apart
+    auto kn = [&](uint32_t d, uint32_t a, uint32_t b, uint32_t bb, int depth, int N) {
+      const uint32_t id = idesc_bf16(128, N, false, true);
+      const uint64_t da = desc_k(sb + a), db = desc_mn(sb + b, bb);
+#pragma unroll
+      for (int ks = 0; ks < depth / 16; ++ks)
+        mma_bf16_ss_elect(tmem + d, desc_step(da, (ks >> 2) * kBlk + (ks & 3) * 32), desc_step(db, ks * 2048), id,
+                          ks > 0);
+    };
+    // A: MN-major (the transposed P tile); B: MN-major
+    auto nn = [&](uint32_t d, uint32_t a, uint32_t b, int N) {
+      const uint32_t id = idesc_bf16(128, N, true, true);
+      const uint64_t da = desc_mn(sb + a, kBlk), db = desc_mn(sb + b, kBlk);
+#pragma unroll
+      for (int ks = 0; ks < C / 16; ++ks)
+        mma_bf16_ss_elect(tmem + d, desc_step(da, ks * 2048), desc_step(db, ks * 2048), id, ks > 0);
+    };
+    bool ok = wait_all(G_QK);
+    if (ok) {
+      tc_fence_after();
+      kk(TG_A, L::Q_OFF, kBlk, L::K_OFF, kBlk, DK, 128, 0);  // Q K^T
+      ok = wait_all(G_VO);
+    }
+    if (ok) {
+      tc_fence_after();
+      kk(TG_B, L::O_OFF, kBlk, L::V_OFF, kBlk, DV, 128, 0);  // dO V^T
+      mma_commit_elect(bar + G_SC);
+      ok = wait_all(G_RH);
+    }
+    if (ok) {
+      tc_fence_after();
+      kn(TG_C, L::K_OFF, L::X_OFF, L::SBLK, DK, DV);  // K R
+      ok = wait_all(G_P);
+    }
+    if (ok) {
+      tc_fence_after();
+      nn(TG_D, L::PA_OFF, L::O_OFF, DV);  // A^T dO
+      mma_commit_elect(bar + G_DV);
+      // dK's parts take the scores' place, which the epilogue has read
+      kk(TG_A, L::V_OFF, kBlk, L::X_OFF, L::SBLK, DV, DK, 0);  // V R^T, hi
+      mma_commit_elect(bar + G_XR);
+      nn(TG_B, L::PB_OFF, L::Q_OFF, DK);  // B^T Q
+      if (GATED) {
+        ok = wait_all(G_RL);
+        if (ok) {
+          tc_fence_after();
+          kk(TG_A, L::V_OFF, kBlk, L::PA_OFF, L::SBLK, DV, DK, 1);  // V R^T, lo
+        }
+      }
+    }
+    if (ok) {
+      mma_commit_elect(bar + G_DK);
+      ok = wait_all(G_ACCFREE) && wait_all(G_SH);  // dV's parts have been read
+    }
+    if (ok) {
+      tc_fence_after();
+      kn(TG_D, L::PB_OFF, L::K_OFF, kBlk, C, DK);              // B K
+      kk(TG_C, L::O_OFF, kBlk, L::X_OFF, L::SBLK, DV, DK, 0);  // dO S^T, hi
+      if (GATED) {
+        ok = wait_all(G_SL);
+        if (ok) {
+          tc_fence_after();
+          kk(TG_C, L::O_OFF, kBlk, L::PA_OFF, L::SBLK, DV, DK, 1);  // dO S^T, lo
+        }
+      }
+    }
+    if (ok) mma_commit_elect(bar + G_DQ);
+    tc_fence_after();  // no MMA may outlive TMEM
+    mma_commit_elect(bar + G_FIN);
+    int zero = 0;
+    const WaitCtl fin{&zero, status, kWaitLimitNs};
+    (void)mbar_wait(bar + G_FIN, 0, fin);
+  } else if (warp >= 4 && warp < 12) {
+    // ----------------------------------------------------------- epilogues --
+    const int row = 32 * w + lane, half = (warp - 4) >> 2;
+    const bool leader = warp == 4 && lane == 0;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
+    float a = 1.f, pre = 1.f, into = 1.f, out = 1.f;
+    if (GATED) {
+      float al[4];
+      load_alpha(alpha, T, c, al);
+      into = decay_into(al, w);
+      out = decay_out(al, w);
+      a = w == 0 ? al[0] : w == 1 ? al[1] : w == 2 ? al[2] : al[3];
+      pre = prefix_product(a);
+      if (half == 0) {
+        suf[row] = suffix_product(a);
+        if (lane == 31) blk[w] = pre;
+        const float gamma = decay_chunk(al);
+        if (leader) thr[8] = gamma;
+      }
+    }
+    // ---- A, B and M's sums ----
+    float fsum = 0.f, esum = 0.f, csum[4] = {0.f, 0.f, 0.f, 0.f};
+    bool ok = named_bar_and(kBarE, 256, wait(G_SC));
+    if (ok) {
+      tc_fence_after();
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int cb = 2 * half + b;
+        float mid = pre, run = 1.f;
+        if (GATED)
+          for (int u = cb + 1; u < w; ++u) mid *= blk[u];
+#pragma unroll
+        for (int pc = 1; pc >= 0; --pc) {  // 16 columns at a time, the right ones first
+          const int c0 = 32 * cb + 16 * pc;
+          uint32_t pa[8], pb[8];
+          if (cb <= w) {
+            uint32_t x[16], y[16];
+            float m[16];
+            tmem_ld16(lanes + TG_A + c0, x);
+            tmem_ld16(lanes + TG_B + c0, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 14; j >= 0; j -= 2) {
+              float va[2], vb[2];
+#pragma unroll
+              for (int h = 1; h >= 0; --h) {
+                const int jj = 16 * pc + j + h;  // column in the block
+                float f = 1.f;
+                if (cb < w) {
+                  if (GATED) f = mid * suf[c0 + j + h];
+                } else {
+                  if (GATED && jj < 31) {
+                    const float t = __shfl_sync(0xffffffffu, a, jj < 31 ? jj + 1 : 31);
+                    run = jj < lane ? run * t : 1.f;
+                  }
+                  f = run;
+                }
+                const bool in = cb < w || jj <= lane;
+                const float s = __uint_as_float(x[j + h]), o = __uint_as_float(y[j + h]);
+                va[h] = in ? s * f : 0.f;
+                vb[h] = in ? o * f : 0.f;
+                m[j + h] = cb < w || jj < lane ? s * vb[h] : 0.f;
+                if (GATED) fsum += m[j + h];
+              }
+              pa[j / 2] = pack2_bf16(va[0], va[1]);
+              pb[j / 2] = pack2_bf16(vb[0], vb[1]);
+            }
+            if (GATED) csum[2 * b + pc] = fold16(m);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) pa[i] = pb[i] = 0;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int col = c0 + 8 * h;
+            const uint32_t at = (uint32_t)(col >> 6) * kBlk + sw128_off(row, (col >> 3) & 7);
+            *reinterpret_cast<uint4*>(sm + L::PA_OFF + at) = make_uint4(pa[4 * h], pa[4 * h + 1], pa[4 * h + 2], pa[4 * h + 3]);
+            *reinterpret_cast<uint4*>(sm + L::PB_OFF + at) = make_uint4(pb[4 * h], pb[4 * h + 1], pb[4 * h + 2], pb[4 * h + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      fence_proxy_async_smem();
+      arrive(G_P);
+      // ---- dV, staged over A ----
+      ok = named_bar_and(kBarE, 256, wait(G_DV));
+    }
+    if (ok) {
+      tc_fence_after();
+      grad_row<DV / 2, false>(lanes + TG_C, lanes + TG_D, out, nullptr, sm + L::PA_OFF, row, half * (DV / 2));
+      tc_fence_before();
+      arrive(G_ACCFREE);
+      fence_proxy_async_smem();
+      named_bar_sync(kBarE, 256);
+      if (leader) {
+#pragma unroll
+        for (int i = 0; i < VB; ++i) tma_store_3d(&tmDV, sb + L::PA_OFF + i * kBlk, 64 * i, t0, bh);
+        bulk_commit_group();
+        bulk_wait_group_read<0>();
+        mbar_arrive(bar + G_PAFREE);
+      }
+      __syncwarp();
+      ok = named_bar_and(kBarE, 256, wait(G_DK));
+    }
+    if (ok) {
+      // ---- dK ----
+      tc_fence_after();
+      esum = grad_row<DK / 2, GATED>(lanes + TG_A, lanes + TG_B, out, sm + L::K_OFF, sm + L::DK_OFF, row, half * (DK / 2));
+      fence_proxy_async_smem();
+      named_bar_sync(kBarE, 256);
+      if (leader) {
+#pragma unroll
+        for (int i = 0; i < KB; ++i) tma_store_3d(&tmDK, sb + L::DK_OFF + i * kBlk, 64 * i, t0, bh);
+        bulk_commit_group();
+      }
+      __syncwarp();
+      ok = named_bar_and(kBarE, 256, wait(G_DQ));
+    }
+    if (ok) {
+      // ---- dQ, staged over Q (each thread over what it has read) ----
+      tc_fence_after();
+      fsum += grad_row<DK / 2, GATED>(lanes + TG_C, lanes + TG_D, into, sm + L::Q_OFF, sm + L::Q_OFF, row, half * (DK / 2));
+      if (GATED) {  // dO has been read
+        reinterpret_cast<float*>(sm + L::FSUM)[half * C + row] = fsum;
+        reinterpret_cast<float*>(sm + L::ESUM)[half * C + row] = esum;
+        if (lane < 16) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            reinterpret_cast<float*>(sm + L::CSUM)[w * C + 64 * half + 16 * i + fold16_col(lane)] = csum[i];
+        }
+        arrive(G_DOTS);
+      }
+      fence_proxy_async_smem();
+      named_bar_sync(kBarE, 256);
+      if (leader) {
+#pragma unroll
+        for (int i = 0; i < KB; ++i) tma_store_3d(&tmDQ, sb + L::Q_OFF + i * kBlk, 64 * i, t0, bh);
+        bulk_commit_group();
+      }
+    }
+    if (leader) bulk_wait_group_all();
+  } else if (GATED && warp >= 12) {
+    // ------------------------------------------------- <S, R> and the sums --
+    constexpr int NP = (int)(L::STATE / 16 / 256);  // 16-byte pieces of a state tile to a thread
+    const int i0 = tid - 12 * 32;
+    float r[NP][8], dot = 0.f;
+    auto piece = [&](uint32_t tile, int i, float (&x)[8]) {
+      unpack_bf16x8(*reinterpret_cast<const uint4*>(sm + tile + 16 * (i0 + 256 * i)), x);
+    };
+    bool ok = wait_all(G_RH);
+    if (ok) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) piece(L::X_OFF, i, r[i]);
+      arrive(G_RHREAD);
+      ok = wait_all(G_RL);
+    }
+    if (ok) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        float x[8];
+        piece(L::PA_OFF, i, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[i][e] += x[e];
+      }
+      arrive(G_RLREAD);
+    }
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      ok = ok && wait_all(part ? G_SL : G_SH);
+      if (ok) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          float x[8];
+          piece(part ? L::PA_OFF : L::X_OFF, i, x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dot = fmaf(x[e], r[i][e], dot);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (lane == 0) thr[warp - 12] = dot;
+    ok = named_bar_and(kBarT, 256, ok && wait(G_DOTS));
+    if (ok && dlog_alpha && warp == 12) {  // four tokens to a lane
+      float sr = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sr += thr[i];
+      sr *= thr[8];
+      const float* F = reinterpret_cast<const float*>(sm + L::FSUM);
+      const float* E = reinterpret_cast<const float*>(sm + L::ESUM);
+      const float* S = reinterpret_cast<const float*>(sm + L::CSUM);
+      float f[4], e[4];
+#pragma unroll
+      for (int k = 3; k >= 0; --k) {  // suffix sums of the lane's own tokens
+        const int t = 4 * lane + k;
+        f[k] = F[t] + F[C + t] - (S[t] + S[C + t] + S[2 * C + t] + S[3 * C + t]) + (k < 3 ? f[k + 1] : 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) e[k] = E[4 * lane + k] + E[C + 4 * lane + k] + (k > 0 ? e[k - 1] : 0.f);
+      float suff = f[0], pref = e[3];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float x = __shfl_down_sync(0xffffffffu, suff, o), y = __shfl_up_sync(0xffffffffu, pref, o);
+        if (lane + o < 32) suff += x;
+        if (lane >= o) pref += y;
+      }
+      suff = __shfl_down_sync(0xffffffffu, suff, 1);  // tokens of later lanes
+      pref = __shfl_up_sync(0xffffffffu, pref, 1);    // of earlier ones
+      if (lane == 31) suff = 0.f;
+      if (lane == 0) pref = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int t = t0 + 4 * lane + k;
+        // no path crosses a wipe: its derivative is 0, not the sums' rounding
+        if (t < T)
+          dlog_alpha[(size_t)bh * T + t] =
+              alpha[t] == 0.f ? 0.f : f[k] + suff + pref + (k > 0 ? e[k - 1] : 0.f) + sr;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+}
+
 template <int DK, bool GATED>
 cudaError_t launch_out(const GatedProblem& p, const GatedScan& s, cudaStream_t st) {
   CUtensorMap mq, mk, mv, mo;
@@ -824,7 +1316,62 @@ cudaError_t fwd(const GatedProblem& p, cudaStream_t st) {
   return launch_out<DK, GATED>(p, s, st);
 }
 
+template <int DK, int DV, bool GATED>
+cudaError_t launch_grad(const GatedProblem& p, const void* S, const void* R, cudaStream_t st) {
+  const int BH = p.B * p.H, nch = (p.T + C - 1) / C;
+  CUtensorMap mq, mk, mv, mo, ms, mr, mdq, mdk, mdv;
+  if (!make_tmap_3d_bf16(&mq, p.q, DK, p.T, BH, C) || !make_tmap_3d_bf16(&mk, p.k, DK, p.T, BH, C) ||
+      !make_tmap_3d_bf16(&mv, p.v, DV, p.T, BH, C) || !make_tmap_3d_bf16(&mo, p.dO, DV, p.T, BH, C) ||
+      !make_tmap_3d_bf16(&ms, S, DV, DK, 2 * BH * nch, DK) || !make_tmap_3d_bf16(&mr, R, DV, DK, 2 * BH * nch, DK) ||
+      !make_tmap_3d_bf16(&mdq, p.dq, DK, p.T, BH, C) || !make_tmap_3d_bf16(&mdk, p.dk, DK, p.T, BH, C) ||
+      !make_tmap_3d_bf16(&mdv, p.dv, DV, p.T, BH, C))
+    return cudaErrorInvalidValue;
+  auto kern = gated_grad_kernel<DK, DV, GATED>;
+  constexpr int smem = (int)GradLayout<DK, DV>::ALLOC;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)((size_t)BH * nch), GATED ? kGradThreads : kGradPlain, smem, st>>>(
+      mq, mk, mv, mo, ms, mr, mdq, mdk, mdv, p.alpha, p.dlog_alpha, p.T, p.status);
+  return cudaGetLastError();
+}
+
+// The workspace of the gradient: the segments' states of both scans, then S
+// and R of every chunk as bf16 hi and lo.
+template <int DK, bool GATED>
+cudaError_t bwd(const GatedProblem& p, cudaStream_t st) {
+  const int BH = p.B * p.H, nch = (p.T + C - 1) / C;
+  const size_t seg = gated_segment_bytes(BH, p.G, DK, p.Dv), sblk = (size_t)DK * p.Dv;
+  uint8_t* ws = static_cast<uint8_t*>(p.scratch);
+  uint8_t* S = ws + 2 * seg;
+  uint8_t* R = S + (size_t)BH * nch * 2 * sblk * 2;
+  GatedScan f = gated_scan_of(p, ws), r = gated_scan_of(p, ws + seg);
+  f.S_in = p.S0;
+  r.S_in = p.dS_T;
+  r.S_out = p.dS0;
+  f.S_in_stride = r.S_in_stride = sblk;
+  cudaError_t e = cudaSuccess;
+  if (p.G > 1) {
+    GatedScan f0 = f;  // S_out of the scan is the caller's only in the forward
+    f0.S_in = nullptr;
+    e = launch_state<DK, GATED, false, false>(p.k, p.v, nullptr, BH, f0, st);
+    if (e == cudaSuccess) e = launch_state<DK, GATED, true, false>(p.q, p.dO, nullptr, BH, r, st);
+  }
+  if (e == cudaSuccess) e = launch_state<DK, GATED, false, true>(p.k, p.v, S, BH, f, st);
+  if (e == cudaSuccess) e = launch_state<DK, GATED, true, true>(p.q, p.dO, R, BH, r, st);
+  if (e != cudaSuccess) return e;
+  return p.Dv == 128 ? launch_grad<DK, 128, GATED>(p, S, R, st) : launch_grad<DK, 64, GATED>(p, S, R, st);
+}
+
 }  // namespace
+
+size_t gated_bwd_bytes(int BH, int T, int G, int Dk, int Dv) {
+  return 2 * gated_segment_bytes(BH, G, Dk, Dv) + (size_t)BH * ((T + C - 1) / C) * 2 * 2 * Dk * Dv * 2;
+}
+
+cudaError_t launch_gated_tc_bwd(const GatedProblem& p, cudaStream_t st) {
+  if (p.alpha) return p.Dk == 128 ? bwd<128, true>(p, st) : bwd<64, true>(p, st);
+  return p.Dk == 128 ? bwd<128, false>(p, st) : bwd<64, false>(p, st);
+}
 
 // Segments: enough for one CTA on every SM, where the state part run twice
 // (about half a chunk's cost each time, and some three chunks of launch and

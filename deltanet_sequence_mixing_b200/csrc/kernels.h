@@ -172,7 +172,10 @@ struct GatedScan {
 // The split of T into G segments of seg_chunks chunks (the last may be shorter).
 void gated_segments(int BH, int T, int Dv, int sms, int* G, int* seg_chunks);
 size_t gated_segment_bytes(int BH, int G, int Dk, int Dv);
+// Scratch of the bf16 gradient.
+size_t gated_bwd_bytes(int BH, int T, int G, int Dk, int Dv);
 cudaError_t launch_gated_tc_fwd(const GatedProblem& p, cudaStream_t st);
+cudaError_t launch_gated_tc_bwd(const GatedProblem& p, cudaStream_t st);
 cudaError_t launch_gated_simt_fwd(const GatedProblem& p, cudaStream_t stream);
 cudaError_t launch_gated_simt_bwd(const GatedProblem& p, cudaStream_t stream);
 
