@@ -14,16 +14,17 @@
 // Roundings to bf16: the decayed scores (one, as the second product's operand)
 // and the copy of S that Q reads.  The state itself is held to float32: its
 // increment's right operand diag(c) V goes in as two bf16 values (hi + lo, the
-// next 8 bits), side by side as N = 128, whose two halves of the accumulator
-// are added to the float32 state in registers.
+// next 8 bits), both accumulated before the increment meets the float32 state
+// in registers.
 //
 // One CTA per (b, h, segment of the sequence, 64 columns of Dv), one CTA per SM:
-//   warp 0       TMA of K, Q (two stages) and V
-//   warp 1       MMA issue, per chunk c: K^T V~ (c), Q S (c), Q K^T (c+1), P V (c),
-//                so that each product's operands have had the other three's time
-//   warps 4-7    P (c) = scores * D, TMEM to TMEM (P is the A operand there)
-//   warps 8-11   state: S <- gamma S + hi + lo in registers, bf16 tile for Q S
-//   warps 12-15  O (c) = G_i QS + PV to a staging tile, stored by TMA
+//   warp 0       TMA of K, Q (two stages) and V (three)
+//   warps 1, 2   MMA issue: Q K^T (c), P V (c-1) | K^T V~ (c), Q S (c).  Issuing a
+//                chunk's MMAs and waiting for their operands takes one warp longer
+//                than the tensor core needs to run them, so there are two
+//   warps 4-11   P (c) = scores * D, TMEM to TMEM (P is the A operand there),
+//                and O = G_i QS + PV; two warps to 32 rows, half of the columns each
+//   warps 12-15  state: S <- gamma S + hi + lo in registers, bf16 tile for Q S
 //   warps 16-19  V~ (c) = diag(c) V as hi and lo tiles (gated only)
 // C = 128 and full-height MMAs because an SS product of M = 128 reads 4 KB of A
 // for every 16 of K whatever N is: larger chunks spread the state's products
@@ -49,11 +50,11 @@ namespace {
 constexpr int C = kGatedChunk, NV = 64;
 static_assert(C == 128, "four warps of 32 rows");
 constexpr uint32_t kBlk = 16384;  // 128 rows x 128 bytes (64 bf16 columns)
-constexpr int kWarpTma = 0, kWarpMma = 1, kWarpP = 4, kWarpState = 8, kWarpO = 12, kWarpV = 16;
+constexpr int kWarpTma = 0, kWarpMma = 1, kWarpMma2 = 2, kWarpO = 4, kWarpState = 12, kWarpV = 16;
 constexpr int kThreads = 20 * 32;
-constexpr int kBarP = 1, kBarO = 2, kBarS = 3;
-// TMEM columns: scores (and P) [2], increment hi | lo, Q S, P V
-constexpr uint32_t TM_SC = 0, TM_DS = 256, TM_QS = 384, TM_PV = 448;
+constexpr int kBarO = 1, kBarS = 1;
+// TMEM columns: scores, P [2], Q S [2], P V, increment
+constexpr uint32_t TM_SC = 0, TM_P = 128, TM_QS = 256, TM_PV = 384, TM_DS = 448;
 
 // Shared memory of the main kernel.
 template <int DK>
@@ -61,11 +62,10 @@ struct OutLayout {
   static constexpr int KB = DK / 64;
   static constexpr uint32_t K_OFF = 0;                  // [2][KB] blocks
   static constexpr uint32_t Q_OFF = K_OFF + 2 * KB * kBlk;
-  static constexpr uint32_t V_OFF = Q_OFF + 2 * KB * kBlk;  // [2]
-  static constexpr uint32_t VT_OFF = V_OFF + 2 * kBlk;  // hi, lo
+  static constexpr uint32_t V_OFF = Q_OFF + 2 * KB * kBlk;  // [3]
+  static constexpr uint32_t VT_OFF = V_OFF + 3 * kBlk;  // hi, lo
   static constexpr uint32_t S_OFF = VT_OFF + 2 * kBlk;  // DK rows x 128 bytes
-  static constexpr uint32_t O_OFF = S_OFF + DK * 128;
-  static constexpr uint32_t SUF_OFF = O_OFF + kBlk;     // [2][128] floats, then [2][4] block products
+  static constexpr uint32_t SUF_OFF = S_OFF + DK * 128;  // [2][128] floats, then [2][4] block products
   static constexpr uint32_t BAR_OFF = SUF_OFF + 2 * 512 + 32;
   static constexpr uint32_t BYTES = BAR_OFF + 256;
   static constexpr uint32_t ALLOC = BYTES + 1024;
@@ -86,15 +86,42 @@ struct StateLayout {
   static_assert(ALLOC <= 232448, "shared memory budget");
 };
 
-// mbarriers (8 bytes each), two per name: chunk parity
+// mbarriers (8 bytes each), two per name (chunk parity; B_FIN: one per issuer),
+// three for B_FULLV and B_VFREE (stage).  A parity can only be told from the one
+// before it, so whoever waits for a phase must stand between it and the next but one
 enum : uint32_t {
-  B_FULLQK = 0, B_FULLV = 16, B_SC = 32, B_P = 48, B_VT = 64, B_DS = 80, B_DSFREE = 96, B_S = 112,
-  B_QS = 128, B_PV = 144, B_OFREE = 160, B_FIN = 176, B_TMEM = 184, B_ABORT = 188
+  B_FULLK = 0, B_FULLQ = 16, B_FULLV = 32, B_SC = 56, B_P = 72, B_VT = 88, B_DS = 104, B_DSFREE = 120, B_S = 136,
+  B_QS = 152, B_PV = 168, B_OFREE = 184, B_VFREE = 200, B_FIN = 224, B_TMEM = 240, B_ABORT = 244
 };
-// of the state kernel: B_XFULL and B_XFREE one per stage
+// of the state kernel: C_FULL and C_FREE one per stage
 enum : uint32_t {
   C_FULL = 0, C_FREE = 24, C_VT = 48, C_DS = 64, C_DSFREE = 80, C_FIN = 96, C_TMEM = 104, C_ABORT = 108
 };
+
+// mbar_wait made short, its limit in polls instead of nanoseconds.  The roles of
+// a kernel run different code at the same time and wait at some twenty places;
+// where their loops together outgrow the SM's instruction cache, every warp
+// stalls on fetches (the main kernel's chunks took 2.1 us on the SMs nearest
+// their code and 3.3 us on the farthest).  A poll sleeps until the phase
+// completes or the hint runs out, so 2^15 of them are some seconds; polls that
+// return at once are still a millisecond, a hundred times the longest wait of a
+// running pipeline.
+__device__ __noinline__ void give_up(volatile int* abort_flag, unsigned int* status) {
+  *abort_flag = 1;
+  if (status) atomicOr(status, kStatusTimeoutBit);
+}
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const WaitCtl& w) {
+  int polls = 32768;
+#pragma unroll 1
+  while (!mbar_try_wait_suspend(bar, parity)) {
+    if (*w.abort_flag) return false;
+    if (--polls == 0) {
+      give_up(w.abort_flag, w.status);
+      return false;
+    }
+  }
+  return true;
+}
 
 // The alphas of chunk c that a lane needs: tokens 32 k + lane of each block k (1 past T).
 __device__ __forceinline__ void load_alpha(const float* alpha, int T, int c, float (&a)[4]) {
@@ -133,34 +160,29 @@ __device__ __forceinline__ float suffix_product(float a) {
 }
 // G_i of the warp's row i = 32 w + lane; c_j of row j.
 __device__ __forceinline__ float decay_into(const float (&a)[4], int w) {
-  float x = prefix_product(w == 0 ? a[0] : w == 1 ? a[1] : w == 2 ? a[2] : a[3]);
-#pragma unroll
-  for (int u = 0; u < 3; ++u) {
-    const float b = warp_product(a[u]);
-    if (u < w) x *= b;
-  }
-  return x;
+  const float x = prefix_product(w == 0 ? a[0] : w == 1 ? a[1] : w == 2 ? a[2] : a[3]);
+  // blocks before this one, as one product per lane
+  return x * warp_product((w > 0 ? a[0] : 1.f) * (w > 1 ? a[1] : 1.f) * (w > 2 ? a[2] : 1.f));
 }
 __device__ __forceinline__ float decay_out(const float (&a)[4], int w) {
-  float x = suffix_product(w == 0 ? a[0] : w == 1 ? a[1] : w == 2 ? a[2] : a[3]);
-#pragma unroll
-  for (int u = 1; u < 4; ++u) {
-    const float b = warp_product(a[u]);
-    if (u > w) x *= b;
-  }
-  return x;
+  const float x = suffix_product(w == 0 ? a[0] : w == 1 ? a[1] : w == 2 ? a[2] : a[3]);
+  return x * warp_product((w < 1 ? a[1] : 1.f) * (w < 2 ? a[2] : 1.f) * (w < 3 ? a[3] : 1.f));
 }
 __device__ __forceinline__ float decay_chunk(const float (&a)[4]) {
   return warp_product(a[0] * a[1] * a[2] * a[3]);
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// 32 bytes to global memory (32-byte aligned).
+__device__ __forceinline__ void st_global32(void* dst, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(reinterpret_cast<uint64_t>(dst)), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 __device__ __forceinline__ float lo_half(uint32_t w) { return __uint_as_float(w << 16); }
@@ -178,23 +200,32 @@ __device__ __forceinline__ void split8(const float* x, uint4& hi, uint4& lo) {
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// Row `row` of a 64-column tile scaled by f into the hi and lo tiles.
+// Row `row` of a 64-column tile scaled by f into the hi and lo tiles, in bf16
+// arithmetic: with f = f_hi + f_lo (bf16 each, 2^-17 left behind), hi = v f_hi
+// rounded, v f_hi - hi fits bf16 exactly (a product of two 8-bit significands
+// has 16 bits), and lo = that + v f_lo: three instructions for two values.
 __device__ __forceinline__ void scale_row(const uint8_t* tile, uint8_t* hi, uint8_t* lo, int row, float f) {
-#pragma unroll
+  const uint32_t fh = pack2_bf16(f, f);
+  const float rest = f - lo_half(fh);
+  const uint32_t fl = pack2_bf16(rest, rest);
+  constexpr uint32_t kNegZero = 0x80008000u;  // v f + (-0) = v f, its sign kept
+#pragma unroll 1
   for (int c0 = 0; c0 < 8; c0 += 4) {
     uint4 u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const uint4*>(tile + sw128_off(row, c0 + i));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float x[8];
-      unpack_bf16x8(u[i], x);
+      const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+      uint32_t h[4], l[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= f;
-      uint4 h, l;
-      split8(x, h, l);
-      *reinterpret_cast<uint4*>(hi + sw128_off(row, c0 + i)) = h;
-      *reinterpret_cast<uint4*>(lo + sw128_off(row, c0 + i)) = l;
+      for (int e = 0; e < 4; ++e) {
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(h[e]) : "r"(v[e]), "r"(fh), "r"(kNegZero));
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(l[e]) : "r"(v[e]), "r"(fh), "r"(h[e] ^ 0x80008000u));
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(l[e]) : "r"(v[e]), "r"(fl), "r"(l[e]));
+      }
+      *reinterpret_cast<uint4*>(hi + sw128_off(row, c0 + i)) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(lo + sw128_off(row, c0 + i)) = make_uint4(l[0], l[1], l[2], l[3]);
     }
   }
 }
@@ -231,22 +262,17 @@ __device__ __forceinline__ void leave_state(float* dst, const float (&s)[NV]) {
     *reinterpret_cast<float4*>(dst + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
 }
 
-// s <- gamma s + this lane's increment (its hi and lo halves at taddr, + 64)
+// s <- gamma s + this lane's increment
 template <bool GATED>
 __device__ __forceinline__ void add_increment(float (&s)[NV], float gamma, uint32_t taddr) {
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
-    uint32_t x[16], y[16];
+    uint32_t x[16];
     tmem_ld16(taddr + 16 * h, x);
-    if (GATED) tmem_ld16(taddr + 64 + 16 * h, y);
     tmem_wait_ld();
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      if (GATED)
-        s[16 * h + e] = fmaf(gamma, s[16 * h + e], __uint_as_float(x[e]) + __uint_as_float(y[e]));
-      else
-        s[16 * h + e] += __uint_as_float(x[e]);
-    }
+    for (int e = 0; e < 16; ++e)
+      s[16 * h + e] = GATED ? fmaf(gamma, s[16 * h + e], __uint_as_float(x[e])) : s[16 * h + e] + __uint_as_float(x[e]);
   }
 }
 
@@ -254,8 +280,7 @@ __device__ __forceinline__ void add_increment(float (&s)[NV], float gamma, uint3
 template <int DK, bool GATED>
 __global__ void __launch_bounds__(kThreads, 1)
     gated_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
-                     const GatedScan p) {
+                     const __grid_constant__ CUtensorMap tmV, __nv_bfloat16* o_all, const GatedScan p) {
   using L = OutLayout<DK>;
   constexpr int KB = L::KB;
   extern __shared__ uint8_t smem_raw[];
@@ -273,10 +298,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (uint32_t i = 0; i < 2; ++i) {
-      for (uint32_t b : {B_FULLQK, B_FULLV, B_SC, B_DS, B_QS, B_PV}) mbar_init(bar + b + 8 * i, 1);
-      for (uint32_t b : {B_P, B_VT, B_DSFREE, B_S, B_OFREE}) mbar_init(bar + b + 8 * i, 4);  // one arrival per warp
+      for (uint32_t b : {B_FULLK, B_FULLQ, B_SC, B_DS, B_QS, B_PV}) mbar_init(bar + b + 8 * i, 1);
+      for (uint32_t b : {B_VT, B_DSFREE, B_S}) mbar_init(bar + b + 8 * i, 4);  // one arrival per warp
+      for (uint32_t b : {B_P, B_OFREE}) mbar_init(bar + b + 8 * i, 8);
+    }
+    for (uint32_t i = 0; i < 3; ++i) {
+      mbar_init(bar + B_FULLV + 8 * i, 1);
+      mbar_init(bar + B_VFREE + 8 * i, 1);
     }
     mbar_init(bar + B_FIN, 1);
+    mbar_init(bar + B_FIN + 8, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -290,8 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = warp_uniform(*tmem_slot);
   const WaitCtl wc{abort_flag, p.status, kWaitLimitNs};
   const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
-  auto full = [&](uint32_t b, int c) { return mbar_wait(bar + b + 8 * (c & 1), (c >> 1) & 1, wc); };
-  auto wait_all = [&](uint32_t b, int c) { return __all_sync(0xffffffffu, full(b, c)) != 0; };
+  auto done = [&](uint32_t b, int c) { return wait_bar(bar + b + 8 * (c & 1), (c >> 1) & 1, wc); };
+  auto full_v = [&](int c) { return wait_bar(bar + B_FULLV + 8 * (c % 3), (c / 3) & 1, wc); };
+  auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
   auto arrive = [&](uint32_t b, int c) {  // one arrival for the warp, after all its lanes
     __syncwarp();
     if (lane == 0) mbar_arrive(bar + b + 8 * (c & 1));
@@ -303,29 +335,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       prefetch_tmap(&tmQ);
       prefetch_tmap(&tmK);
       prefetch_tmap(&tmV);
-      int qk = 0, v = 0;  // issued
+      int nk = 0, nq = 0, nv = 0;  // issued
       for (int c = 0; c < n; ++c) {
         const int s = c & 1, row = (first + c) * C;
-        // K (c-2) was last read by its increment, Q by Q S, V by P V
-        if (c >= 2 && !(full(B_DS, c - 2) && full(B_QS, c - 2))) break;
-        mbar_expect_tx(bar + B_FULLQK + 8 * s, 2 * KB * kBlk);
+        // P V (c-3) has read the stage (and so has K^T V or V~: K (c-1) waited for the increment)
+        if (c >= 3 && !wait_bar(bar + B_VFREE + 8 * (c % 3), (c / 3 - 1) & 1, wc)) break;
+        mbar_expect_tx(bar + B_FULLV + 8 * (c % 3), kBlk);
+        tma_load_3d(sb + L::V_OFF + (c % 3) * kBlk, &tmV, bar + B_FULLV + 8 * (c % 3), j0, row, bh);
+        nv = c + 1;
+        if (c >= 2 && !(done(B_DS, c - 2) && done(B_SC, c - 2))) break;
+        mbar_expect_tx(bar + B_FULLK + 8 * s, KB * kBlk);
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-          tma_load_3d(sb + L::K_OFF + (s * KB + kb) * kBlk, &tmK, bar + B_FULLQK + 8 * s, kb * 64, row, bh);
-          tma_load_3d(sb + L::Q_OFF + (s * KB + kb) * kBlk, &tmQ, bar + B_FULLQK + 8 * s, kb * 64, row, bh);
-        }
-        qk = c + 1;
-        if (c >= 2 && !full(B_PV, c - 2)) break;
-        mbar_expect_tx(bar + B_FULLV + 8 * s, kBlk);
-        tma_load_3d(sb + L::V_OFF + s * kBlk, &tmV, bar + B_FULLV + 8 * s, j0, row, bh);
-        v = c + 1;
+        for (int kb = 0; kb < KB; ++kb)
+          tma_load_3d(sb + L::K_OFF + (s * KB + kb) * kBlk, &tmK, bar + B_FULLK + 8 * s, kb * 64, row, bh);
+        nk = c + 1;
+        if (c >= 2 && !done(B_QS, c - 2)) break;
+        mbar_expect_tx(bar + B_FULLQ + 8 * s, KB * kBlk);
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+          tma_load_3d(sb + L::Q_OFF + (s * KB + kb) * kBlk, &tmQ, bar + B_FULLQ + 8 * s, kb * 64, row, bh);
+        nq = c + 1;
       }
       int zero = 0;  // never leave with copies in flight
       const WaitCtl drain{&zero, p.status, kWaitLimitNs};
-      for (int c = qk > 2 ? qk - 2 : 0; c < qk; ++c) (void)mbar_wait(bar + B_FULLQK + 8 * (c & 1), (c >> 1) & 1, drain);
-      for (int c = v > 2 ? v - 2 : 0; c < v; ++c) (void)mbar_wait(bar + B_FULLV + 8 * (c & 1), (c >> 1) & 1, drain);
+      for (int c = nk > 2 ? nk - 2 : 0; c < nk; ++c) (void)wait_bar(bar + B_FULLK + 8 * (c & 1), (c >> 1) & 1, drain);
+      for (int c = nq > 2 ? nq - 2 : 0; c < nq; ++c) (void)wait_bar(bar + B_FULLQ + 8 * (c & 1), (c >> 1) & 1, drain);
+      for (int c = nv > 3 ? nv - 3 : 0; c < nv; ++c) (void)wait_bar(bar + B_FULLV + 8 * (c % 3), (c / 3) & 1, drain);
     }
-  } else if (warp == kWarpMma) {
+  } else if (warp == kWarpMma || warp == kWarpMma2) {
     // ------------------------------------------------------------------ MMA --
     auto scores = [&](int c) {
       constexpr uint32_t id = idesc_bf16(128, 128, false, false);
@@ -334,19 +371,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int ks = 0; ks < DK / 16; ++ks) {
         const uint32_t off = (ks >> 2) * kBlk + (ks & 3) * 32;
-        mma_bf16_ss_elect(tmem + TM_SC + 128 * (c & 1), desc_step(dq, off), desc_step(dk, off), id, ks > 0);
+        mma_bf16_ss_elect(tmem + TM_SC, desc_step(dq, off), desc_step(dk, off), id, ks > 0);
       }
       mma_commit_elect(bar + B_SC + 8 * (c & 1));
     };
-    // K^T [hi | lo] (gated) or K^T V; with DK = 64 the product's upper 64 rows
+    // K^T hi + K^T lo (gated) or K^T V; with DK = 64 the product's upper 64 rows
     // are computed from the next block and never read
     auto increment = [&](int c) {
-      constexpr uint32_t id = idesc_bf16(128, GATED ? 128 : 64, true, true);
+      constexpr uint32_t id = idesc_bf16(128, 64, true, true);
       const uint64_t da = desc_mn(sb + L::K_OFF + (c & 1) * KB * kBlk, kBlk);
-      const uint64_t db = desc_mn(sb + (GATED ? L::VT_OFF : L::V_OFF + (c & 1) * kBlk), kBlk);
+      const uint64_t db = desc_mn(sb + (GATED ? L::VT_OFF : L::V_OFF + (c % 3) * kBlk), kBlk);
 #pragma unroll
-      for (int ks = 0; ks < C / 16; ++ks)
-        mma_bf16_ss_elect(tmem + TM_DS, desc_step(da, ks * 2048), desc_step(db, ks * 2048), id, ks > 0);
+      for (int ks = 0; ks < (GATED ? 2 : 1) * C / 16; ++ks)
+        mma_bf16_ss_elect(tmem + TM_DS, desc_step(da, (ks & 7) * 2048), desc_step(db, ks * 2048), id, ks > 0);
       mma_commit_elect(bar + B_DS + 8 * (c & 1));
     };
     auto read_state = [&](int c) {
@@ -354,122 +391,167 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dq = desc_k(sb + L::Q_OFF + (c & 1) * KB * kBlk), ds = desc_mn(sb + L::S_OFF, kBlk);
 #pragma unroll
       for (int ks = 0; ks < DK / 16; ++ks)
-        mma_bf16_ss_elect(tmem + TM_QS, desc_step(dq, (ks >> 2) * kBlk + (ks & 3) * 32), desc_step(ds, ks * 2048), id,
+        mma_bf16_ss_elect(tmem + TM_QS + 64 * (c & 1), desc_step(dq, (ks >> 2) * kBlk + (ks & 3) * 32), desc_step(ds, ks * 2048), id,
                           ks > 0);
       mma_commit_elect(bar + B_QS + 8 * (c & 1));
     };
     auto inner = [&](int c) {
       constexpr uint32_t id = idesc_bf16(128, 64, false, true);
-      const uint64_t dv = desc_mn(sb + L::V_OFF + (c & 1) * kBlk, kBlk);
+      const uint64_t dv = desc_mn(sb + L::V_OFF + (c % 3) * kBlk, kBlk);
 #pragma unroll
       for (int ks = 0; ks < C / 16; ++ks)
-        mma_bf16_ts_elect(tmem + TM_PV, tmem + TM_SC + 128 * (c & 1) + 8 * ks, desc_step(dv, ks * 2048), id, ks > 0);
+        mma_bf16_ts_elect(tmem + TM_PV, tmem + TM_P + 64 * (c & 1) + 8 * ks, desc_step(dv, ks * 2048), id, ks > 0);
       mma_commit_elect(bar + B_PV + 8 * (c & 1));
+      mma_commit_elect(bar + B_VFREE + 8 * (c % 3));
     };
-    bool ok = wait_all(B_FULLQK, 0);
-    if (ok) {
-      tc_fence_after();
-      scores(0);
-    }
-    for (int c = 0; c < n && ok; ++c) {
-      ok = wait_all(GATED ? B_VT : B_FULLV, c) && (c < 1 || wait_all(B_DSFREE, c - 1));
-      if (!ok) break;
-      tc_fence_after();
-      increment(c);
-      ok = wait_all(B_S, c) && (c < 1 || wait_all(B_OFREE, c - 1));
-      if (!ok) break;
-      tc_fence_after();
-      read_state(c);
-      if (c + 1 < n) {
-        // scores (c+1) overwrite P (c-1), which P V (c-1) has read
-        ok = wait_all(B_FULLQK, c + 1) && (c < 1 || wait_all(B_PV, c - 1));
+    bool ok = true;
+    if (warp == kWarpMma) {
+      for (int c = 0; c <= n && ok; ++c) {
+        if (c < n) {
+          // P (c-1) has been made of the scores that these overwrite
+          ok = all(done(B_FULLK, c) && done(B_FULLQ, c) && (c < 1 || done(B_P, c - 1)));
+          if (!ok) break;
+          tc_fence_after();
+          scores(c);
+        }
+        if (c >= 1) {
+          ok = all(done(B_P, c - 1) && full_v(c - 1) && (c < 2 || done(B_OFREE, c - 2)));
+          if (!ok) break;
+          tc_fence_after();
+          inner(c - 1);
+        }
+      }
+    } else {
+      for (int c = 0; c < n && ok; ++c) {
+        ok = all(done(B_FULLK, c) && (GATED ? done(B_VT, c) : full_v(c)) && (c < 1 || done(B_DSFREE, c - 1)));
         if (!ok) break;
         tc_fence_after();
-        scores(c + 1);
+        increment(c);
+        ok = all(done(B_FULLQ, c) && done(B_S, c) && (c < 2 || done(B_OFREE, c - 2)));
+        if (!ok) break;
+        tc_fence_after();
+        read_state(c);
       }
-      ok = wait_all(B_P, c) && (GATED ? true : wait_all(B_FULLV, c));
-      if (!ok) break;
-      tc_fence_after();
-      inner(c);
     }
     tc_fence_after();  // no MMA may outlive TMEM
-    mma_commit_elect(bar + B_FIN);
+    const uint32_t fin_bar = bar + B_FIN + (warp == kWarpMma ? 0 : 8);
+    mma_commit_elect(fin_bar);
     int zero = 0;
     const WaitCtl fin{&zero, p.status, kWaitLimitNs};
-    (void)mbar_wait(bar + B_FIN, 0, fin);
-  } else if (warp >= kWarpP && warp < kWarpP + 4) {
-    // -------------------------------------------------------------- scores --
-    float a = 1.f, next = 1.f;
+    (void)wait_bar(fin_bar, 0, fin);
+  } else if (warp >= kWarpO && warp < kWarpO + 8) {
+    // ----------------------------------------------------- scores, outputs --
+    const int half = (warp - kWarpO) >> 2, row = 32 * w + lane;
+    __nv_bfloat16* o_row = o_all + (size_t)bh * T * p.Dv + j0 + 32 * half;
+    float* suf = reinterpret_cast<float*>(sm + L::SUF_OFF);
+    float* blk = reinterpret_cast<float*>(sm + L::SUF_OFF + 1024);
+    float a = 1.f, pre = 1.f, into = 1.f, ahead = 1.f;
     auto load = [&](int c) {
-      const int t = (first + c) * C + 32 * w + lane;
-      return GATED && t < T ? __ldg(alpha + t) : 1.f;
+      const int t = (first + c) * C + row;
+      return GATED && c < n && t < T ? __ldg(alpha + t) : 1.f;
     };
-    next = load(0);
+    auto factors = [&](int c) {  // chunk c's, into buffer c & 1
+      a = ahead;
+      ahead = load(c + 1);
+      pre = prefix_product(a);
+      if (half == 0) {
+        suf[(c & 1) * C + row] = suffix_product(a);
+        if (lane == 31) blk[(c & 1) * 4 + w] = pre;
+      }
+    };
+    ahead = load(0);
+    if (GATED) factors(0);
     bool ok = true;
-    for (int c = 0; c < n && ok; ++c) {
-      a = next;
-      if (c + 1 < n) next = load(c + 1);
-      float pre = 1.f, mid = 1.f;
-      float* suf = reinterpret_cast<float*>(sm + L::SUF_OFF) + (c & 1) * C;
-      float* blk = reinterpret_cast<float*>(sm + L::SUF_OFF + 1024) + (c & 1) * 4;
-      if (GATED) {
-        pre = prefix_product(a);
-        suf[32 * w + lane] = suffix_product(a);
-        if (lane == 31) blk[w] = pre;
-      }
-      // every warp's factors are in place (and all have left the buffer of chunk c-2)
-      ok = named_bar_and(kBarP, 128, full(B_SC, c));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t sc = lanes + TM_SC + 128 * (c & 1);
-      // column blocks from the diagonal down, then zeros above it: block cb is
-      // read before P overwrites it (P's columns 16 cb .. of the same lanes)
-      uint32_t d[16];
+    // the eight warps meet once a chunk, so one that gives up says so there
+    for (int c = 0; c <= n; ++c) {
+      const float into_before = into;
+      if (c < n) {
+        // every warp's factors are in place (and all have left the buffer of
+        // chunk c-1); P V (c-2) has read the P that this one overwrites
+        ok = named_bar_and(kBarO, 256, ok && done(B_SC, c) && (c < 2 || done(B_PV, c - 2)));
+        if (!ok) break;
+        tc_fence_after();
+        const float* sf = suf + (c & 1) * C;
+        const float* bl = blk + (c & 1) * 4;
+        const uint32_t pt = lanes + TM_P + 64 * (c & 1);
+        float run = 1.f;
 #pragma unroll 1
-      for (int cb = 0; cb < 4; ++cb) {
-        if (cb > w) {
+        for (int pc = 3; pc >= 0; --pc) {  // 16 columns at a time, the right ones first
+          const int c0 = 64 * half + 16 * pc, cb = c0 >> 5;
+          uint32_t d[8];
+          if (cb > w) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) d[i] = 0;
-        } else {
-          uint32_t x[32];
-          tmem_ld32(sc + 32 * cb, x);
-          if (cb < w) {
-            if (GATED) {
-              mid = pre;
-              for (int u = cb + 1; u < w; ++u) mid *= blk[u];
-            }
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
-              if (GATED) f = *reinterpret_cast<const float4*>(suf + 32 * cb + j);
-              if (GATED) { f.x *= mid; f.y *= mid; f.z *= mid; f.w *= mid; }
-              d[j / 2] = pack2_bf16(__uint_as_float(x[j]) * f.x, __uint_as_float(x[j + 1]) * f.y);
-              d[j / 2 + 1] = pack2_bf16(__uint_as_float(x[j + 2]) * f.z, __uint_as_float(x[j + 3]) * f.w);
-            }
+            for (int i = 0; i < 8; ++i) d[i] = 0;
           } else {
-            tmem_wait_ld();
-            float run = 1.f;
+            uint32_t x[16];
+            float f[16];
+            tmem_ld16(lanes + TM_SC + c0, x);
+            if (GATED && cb < w) {
+              float mid = pre;
+              if (cb + 1 < w) mid *= bl[w - 1];
+              if (cb + 2 < w) mid *= bl[w - 2];
 #pragma unroll
-            for (int j = 30; j >= 0; j -= 2) {  // columns j + 1, then j
-              if (GATED && j < 30) {
-                const float t = __shfl_sync(0xffffffffu, a, j + 2 < 32 ? j + 2 : 31);
-                run = j + 1 < lane ? run * t : 1.f;
+              for (int j = 0; j < 16; j += 4) {
+                const float4 u = *reinterpret_cast<const float4*>(sf + c0 + j);
+                f[j] = u.x * mid; f[j + 1] = u.y * mid; f[j + 2] = u.z * mid; f[j + 3] = u.w * mid;
               }
-              const float hi = j + 1 <= lane ? __uint_as_float(x[j + 1]) * run : 0.f;
-              if (GATED) {
-                const float t = __shfl_sync(0xffffffffu, a, j + 1);
-                run = j < lane ? run * t : 1.f;
+            } else if (GATED) {
+              const int b0 = c0 & 31;  // the block's first column of the piece
+#pragma unroll
+              for (int j = 15; j >= 0; --j) {  // run: the product of alpha over (column, row]
+                const float t = __shfl_sync(0xffffffffu, a, b0 + j + 1);
+                run = b0 + j < lane ? run * t : 1.f;
+                f[j] = run;
               }
-              d[j / 2] = pack2_bf16(j <= lane ? __uint_as_float(x[j]) * run : 0.f, hi);
             }
+            tmem_wait_ld();
+            if (cb == w) {
+              const int top = lane - (c0 & 31);  // columns up to the diagonal
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (j > top) x[j] = 0;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; j += 2)
+              d[j / 2] = GATED ? pack2_bf16(__uint_as_float(x[j]) * f[j], __uint_as_float(x[j + 1]) * f[j + 1])
+                               : pack2_bf16(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
           }
+          tmem_st8(pt + c0 / 2, d);
         }
-        tmem_st16(sc + 16 * cb, d);
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(B_P, c);
+        if (GATED) {
+          into = pre;
+          for (int u = 0; u < w; ++u) into *= bl[u];
+          if (c + 1 < n) factors(c + 1);
+        }
       }
-      tmem_wait_st();
-      tc_fence_before();
-      arrive(B_P, c);
+      if (c >= 1) {
+        ok = all(ok && done(B_QS, c - 1) && done(B_PV, c - 1));
+        if (!ok) continue;
+        tc_fence_after();
+        const int t = (first + c - 1) * C + row;
+        uint32_t r[16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[16], y[16];
+          tmem_ld16(lanes + TM_QS + 64 * ((c - 1) & 1) + 32 * half + 16 * h, x);
+          tmem_ld16(lanes + TM_PV + 32 * half + 16 * h, y);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; e += 2)
+            r[8 * h + e / 2] = pack2_bf16(fmaf(into_before, __uint_as_float(x[e]), __uint_as_float(y[e])),
+                                          fmaf(into_before, __uint_as_float(x[e + 1]), __uint_as_float(y[e + 1])));
+        }
+        tc_fence_before();
+        arrive(B_OFREE, c - 1);
+        if (t < T) {
+          __nv_bfloat16* dst = o_row + (size_t)t * p.Dv;
+          st_global32(dst, r);
+          st_global32(dst + 16, r + 8);
+        }
+      }
     }
   } else if (warp >= kWarpState && warp < kWarpState + 4) {
     // --------------------------------------------------------------- state --
@@ -494,14 +576,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int c = 0; c < n && ok; ++c) {
       const float gamma = GATED ? decay_chunk(a) : 1.f;
       if (GATED && c + 1 < n) load_alpha(alpha, T, first + c + 1, a);
-      ok = wait_all(B_DS, c);
+      ok = all(done(B_DS, c));
       if (!ok) break;
       tc_fence_after();
       add_increment<GATED>(s, gamma, lanes + TM_DS);
       tc_fence_before();
       arrive(B_DSFREE, c);
       if (c + 1 < n) {
-        ok = wait_all(B_QS, c);  // Q S (c) has read the tile
+        ok = all(done(B_QS, c));  // Q S (c) has read the tile
         if (!ok) break;
         put();
         arrive(B_S, c + 1);
@@ -509,47 +591,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (ok && live && p.S_out && g == p.G - 1)
       leave_state(p.S_out + (size_t)bh * DK * p.Dv + (size_t)row * p.Dv + j0, s);
-  } else if (warp >= kWarpO && warp < kWarpO + 4) {
-    // -------------------------------------------------------------- output --
-    const int row = 32 * w + lane;
-    const bool leader = warp == kWarpO && lane == 0;
-    float a[4] = {1.f, 1.f, 1.f, 1.f};
-    if (GATED) load_alpha(alpha, T, first, a);
-    bool ok = true;
-    for (int c = 0; c < n && ok; ++c) {
-      const float into = GATED ? decay_into(a, w) : 1.f;
-      if (GATED && c + 1 < n) load_alpha(alpha, T, first + c + 1, a);
-      if (leader) bulk_wait_group_read<0>();  // the staging tile is free
-      ok = named_bar_and(kBarO, 128, full(B_PV, c) && full(B_QS, c));
-      if (!ok) break;
-      tc_fence_after();
-      uint4 out[8];
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        uint32_t x[16], y[16];
-        tmem_ld16(lanes + TM_QS + 16 * h, x);
-        tmem_ld16(lanes + TM_PV + 16 * h, y);
-        tmem_wait_ld();
-        uint32_t o[8];
-#pragma unroll
-        for (int e = 0; e < 16; e += 2)
-          o[e / 2] = pack2_bf16(fmaf(into, __uint_as_float(x[e]), __uint_as_float(y[e])),
-                                fmaf(into, __uint_as_float(x[e + 1]), __uint_as_float(y[e + 1])));
-        out[2 * h] = make_uint4(o[0], o[1], o[2], o[3]);
-        out[2 * h + 1] = make_uint4(o[4], o[5], o[6], o[7]);
-      }
-      tc_fence_before();
-      arrive(B_OFREE, c);
-#pragma unroll
-      for (int c16 = 0; c16 < 8; ++c16) *reinterpret_cast<uint4*>(sm + L::O_OFF + sw128_off(row, c16)) = out[c16];
-      fence_proxy_async_smem();
-      named_bar_sync(kBarO, 128);
-      if (leader) {
-        tma_store_3d(&tmO, sb + L::O_OFF, j0, (first + c) * C, bh);
-        bulk_commit_group();
-      }
-    }
-    if (leader) bulk_wait_group_all();
   } else if (GATED && warp >= kWarpV) {
     // --------------------------------------------------------- diag(c) V --
     const int row = 32 * w + lane;
@@ -559,9 +600,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int c = 0; c < n && ok; ++c) {
       const float out = decay_out(a, w);
       if (c + 1 < n) load_alpha(alpha, T, first + c + 1, a);
-      ok = wait_all(B_FULLV, c) && (c < 1 || wait_all(B_DS, c - 1));
+      ok = all(full_v(c) && (c < 1 || done(B_DS, c - 1)));
       if (!ok) break;
-      scale_row(sm + L::V_OFF + (c & 1) * kBlk, sm + L::VT_OFF, sm + L::VT_OFF + kBlk, row, out);
+      scale_row(sm + L::V_OFF + (c % 3) * kBlk, sm + L::VT_OFF, sm + L::VT_OFF + kBlk, row, out);
       fence_proxy_async_smem();
       arrive(B_VT, c);
     }
@@ -615,7 +656,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     fence_mbar_init();
   }
   if (warp == kWarpMma) {
-    tmem_alloc(smem_u32(tmem_slot), 256);
+    tmem_alloc(smem_u32(tmem_slot), 128);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -624,9 +665,9 @@ __global__ void __launch_bounds__(kStateThreads, 1)
   const uint32_t tmem = warp_uniform(*tmem_slot);
   const WaitCtl wc{abort_flag, p.status, kWaitLimitNs};
   auto wait2 = [&](uint32_t b, int i) {  // a barrier pair by parity
-    return __all_sync(0xffffffffu, mbar_wait(bar + b + 8 * (i & 1), (i >> 1) & 1, wc)) != 0;
+    return __all_sync(0xffffffffu, wait_bar(bar + b + 8 * (i & 1), (i >> 1) & 1, wc)) != 0;
   };
-  auto wait_stage = [&](uint32_t b, int i) { return mbar_wait(bar + b + 8 * (i % NST), (i / NST) & 1, wc); };
+  auto wait_stage = [&](uint32_t b, int i) { return wait_bar(bar + b + 8 * (i % NST), (i / NST) & 1, wc); };
 
   if (warp == kWarpTma) {
     if (lane == 0) {
@@ -646,7 +687,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
       int zero = 0;  // never leave with copies in flight
       const WaitCtl drain{&zero, p.status, kWaitLimitNs};
       for (int i = issued > NST ? issued - NST : 0; i < issued; ++i)
-        (void)mbar_wait(bar + C_FULL + 8 * (i % NST), (i / NST) & 1, drain);
+        (void)wait_bar(bar + C_FULL + 8 * (i % NST), (i / NST) & 1, drain);
     }
   } else if (warp == kWarpMma) {
     bool ok = true;
@@ -656,12 +697,12 @@ __global__ void __launch_bounds__(kStateThreads, 1)
            (i < 2 || wait2(C_DSFREE, i - 2));
       if (!ok) break;
       tc_fence_after();
-      constexpr uint32_t id = idesc_bf16(128, GATED ? 128 : 64, true, true);
+      constexpr uint32_t id = idesc_bf16(128, 64, true, true);
       const uint64_t da = desc_mn(sb + L::X_OFF + s * KB * kBlk, kBlk);
       const uint64_t db = desc_mn(sb + (GATED ? L::VT_OFF : L::Z_OFF + s * kBlk), kBlk);
 #pragma unroll
-      for (int ks = 0; ks < C / 16; ++ks)
-        mma_bf16_ss_elect(tmem + 128 * b, desc_step(da, ks * 2048), desc_step(db, ks * 2048), id, ks > 0);
+      for (int ks = 0; ks < (GATED ? 2 : 1) * C / 16; ++ks)
+        mma_bf16_ss_elect(tmem + 64 * b, desc_step(da, (ks & 7) * 2048), desc_step(db, ks * 2048), id, ks > 0);
       mma_commit_elect(bar + C_DS + 8 * b);
       mma_commit_elect(bar + C_FREE + 8 * s);
     }
@@ -669,7 +710,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     mma_commit_elect(bar + C_FIN);
     int zero = 0;
     const WaitCtl fin{&zero, p.status, kWaitLimitNs};
-    (void)mbar_wait(bar + C_FIN, 0, fin);
+    (void)wait_bar(bar + C_FIN, 0, fin);
   } else if (warp >= 4 && warp < 8) {
     const int row = 32 * w + lane;
     const bool live = row < DK, leader = warp == 4 && lane == 0;
@@ -716,10 +757,10 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         }
       }
       // with STORE the four warps meet at barriers, so they leave together
-      ok = STORE ? named_bar_and(kBarS, 128, mbar_wait(bar + C_DS + 8 * (i & 1), (i >> 1) & 1, wc)) : wait2(C_DS, i);
+      ok = STORE ? named_bar_and(kBarS, 128, wait_bar(bar + C_DS + 8 * (i & 1), (i >> 1) & 1, wc)) : wait2(C_DS, i);
       if (!ok) break;
       tc_fence_after();
-      add_increment<GATED>(s, gamma, lanes + 128 * (i & 1));
+      add_increment<GATED>(s, gamma, lanes + 64 * (i & 1));
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar + C_DSFREE + 8 * (i & 1));
@@ -754,7 +795,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kWarpMma) tmem_dealloc(tmem, 256);
+  if (warp == kWarpMma) tmem_dealloc(tmem, 128);
 }
 
 // --------------------------------------------------------- gradient kernel --
@@ -892,7 +933,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   tc_fence_after();
   const uint32_t tmem = warp_uniform(*tmem_slot);
   const WaitCtl wc{abort_flag, status, kWaitLimitNs};
-  auto wait = [&](uint32_t b) { return mbar_wait(bar + b, 0, wc); };
+  auto wait = [&](uint32_t b) { return wait_bar(bar + b, 0, wc); };
   auto wait_all = [&](uint32_t b) { return __all_sync(0xffffffffu, wait(b)) != 0; };
   auto arrive = [&](uint32_t b) {
     __syncwarp();
@@ -938,7 +979,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       }
       int zero = 0;  // never leave with copies in flight
       const WaitCtl drain{&zero, status, kWaitLimitNs};
-      for (int i = 0; i < n; ++i) (void)mbar_wait(bar + got[i], 0, drain);
+      for (int i = 0; i < n; ++i) (void)wait_bar(bar + got[i], 0, drain);
     }
   } else if (warp == kWarpMma) {
     // A: K-major tile of 64-column blocks `ab` apart; B: K-major blocks `bb` apart
@@ -1021,7 +1062,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     mma_commit_elect(bar + G_FIN);
     int zero = 0;
     const WaitCtl fin{&zero, status, kWaitLimitNs};
-    (void)mbar_wait(bar + G_FIN, 0, fin);
+    (void)wait_bar(bar + G_FIN, 0, fin);
   } else if (warp >= 4 && warp < 12) {
     // ----------------------------------------------------------- epilogues --
     const int row = 32 * w + lane, half = (warp - 4) >> 2;
@@ -1251,17 +1292,18 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 
 template <int DK, bool GATED>
 cudaError_t launch_out(const GatedProblem& p, const GatedScan& s, cudaStream_t st) {
-  CUtensorMap mq, mk, mv, mo;
+  CUtensorMap mq, mk, mv;
   const int BH = p.B * p.H;
   if (!make_tmap_3d_bf16(&mq, p.q, DK, p.T, BH, C) || !make_tmap_3d_bf16(&mk, p.k, DK, p.T, BH, C) ||
-      !make_tmap_3d_bf16(&mv, p.v, p.Dv, p.T, BH, C) || !make_tmap_3d_bf16(&mo, p.o, p.Dv, p.T, BH, C))
+      !make_tmap_3d_bf16(&mv, p.v, p.Dv, p.T, BH, C))
     return cudaErrorInvalidValue;
   auto kern = gated_out_kernel<DK, GATED>;
   constexpr int smem = (int)OutLayout<DK>::ALLOC;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   // without a gate the scaling warps have nothing to do
-  kern<<<(unsigned)((size_t)BH * s.G * (p.Dv / NV)), GATED ? kThreads : 32 * kWarpV, smem, st>>>(mq, mk, mv, mo, s);
+  kern<<<(unsigned)((size_t)BH * s.G * (p.Dv / NV)), GATED ? kThreads : 32 * kWarpV, smem, st>>>(
+      mq, mk, mv, static_cast<__nv_bfloat16*>(p.o), s);
   return cudaGetLastError();
 }
 
