@@ -14,18 +14,20 @@
 // Roundings to bf16: the decayed scores (one, as the second product's operand)
 // and the copy of S that Q reads.  The state itself is held to float32: its
 // increment's right operand diag(c) V goes in as two bf16 values (hi + lo, the
-// next 8 bits), both accumulated before the increment meets the float32 state
-// in registers.
+// next 8 bits), side by side as N = 128, whose two halves of the accumulator
+// are added to the float32 state in registers.
 //
 // One CTA per (b, h, segment of the sequence, 64 columns of Dv), one CTA per SM:
 //   warp 0       TMA of K, Q (two stages) and V (three)
 //   warps 1, 2   MMA issue: Q K^T (c), P V (c-1) | K^T V~ (c), Q S (c).  Issuing a
 //                chunk's MMAs and waiting for their operands takes one warp longer
 //                than the tensor core needs to run them, so there are two
-//   warps 4-11   P (c) = scores * D, TMEM to TMEM (P is the A operand there),
-//                and O = G_i QS + PV; two warps to 32 rows, half of the columns each
+//   warp 3       the decays of a chunk's rows, ahead
+//   warps 4-11   V~ (c) = diag(c) V as hi and lo tiles, then P (c) = scores * D,
+//                TMEM to TMEM (P is the A operand there); two warps to 32 rows,
+//                half of the columns each
 //   warps 12-15  state: S <- gamma S + hi + lo in registers, bf16 tile for Q S
-//   warps 16-19  V~ (c) = diag(c) V as hi and lo tiles (gated only)
+//   warps 16-19  O (c) = G_i QS + PV
 // C = 128 and full-height MMAs because an SS product of M = 128 reads 4 KB of A
 // for every 16 of K whatever N is: larger chunks spread the state's products
 // over more tokens, and shared-memory bandwidth is what the kernel spends.
@@ -50,11 +52,15 @@ namespace {
 constexpr int C = kGatedChunk, NV = 64;
 static_assert(C == 128, "four warps of 32 rows");
 constexpr uint32_t kBlk = 16384;  // 128 rows x 128 bytes (64 bf16 columns)
-constexpr int kWarpTma = 0, kWarpMma = 1, kWarpMma2 = 2, kWarpO = 4, kWarpState = 12, kWarpV = 16;
+constexpr int kWarpTma = 0, kWarpMma = 1, kWarpMma2 = 2, kWarpDecay = 3, kWarpP = 4, kWarpState = 12, kWarpO = 16;
 constexpr int kThreads = 20 * 32;
-constexpr int kBarO = 1, kBarS = 1;
-// TMEM columns: scores, P [2], Q S [2], P V, increment
-constexpr uint32_t TM_SC = 0, TM_P = 128, TM_QS = 256, TM_PV = 384, TM_DS = 448;
+constexpr int kBarS = 1;
+// TMEM columns: scores [2] (P's halves in columns 0-31 and 64-95 of them), increment hi | lo, Q S, P V
+constexpr uint32_t TM_SC = 0, TM_DS = 256, TM_QS = 384, TM_PV = 448;
+
+// A chunk's decays: the products of the blocks of 32 tokens, and of every token
+// the product over the tokens of its block behind it.
+constexpr uint32_t kDecayBytes = 16 + 4 * C;
 
 // Shared memory of the main kernel.
 template <int DK>
@@ -65,9 +71,9 @@ struct OutLayout {
   static constexpr uint32_t V_OFF = Q_OFF + 2 * KB * kBlk;  // [3]
   static constexpr uint32_t VT_OFF = V_OFF + 3 * kBlk;  // hi, lo
   static constexpr uint32_t S_OFF = VT_OFF + 2 * kBlk;  // DK rows x 128 bytes
-  static constexpr uint32_t SUF_OFF = S_OFF + DK * 128;  // [2][128] floats, then [2][4] block products
-  static constexpr uint32_t BAR_OFF = SUF_OFF + 2 * 512 + 32;
-  static constexpr uint32_t BYTES = BAR_OFF + 256;
+  static constexpr uint32_t SUF_OFF = S_OFF + DK * 128;  // [3]: 4 block products, 128 floats
+  static constexpr uint32_t BAR_OFF = SUF_OFF + 3 * kDecayBytes;
+  static constexpr uint32_t BYTES = BAR_OFF + 272;
   static constexpr uint32_t ALLOC = BYTES + 1024;
   static_assert(ALLOC <= 232448, "shared memory budget");
 };
@@ -87,36 +93,33 @@ struct StateLayout {
 };
 
 // mbarriers (8 bytes each), two per name (chunk parity; B_FIN: one per issuer),
-// three for B_FULLV and B_VFREE (stage).  A parity can only be told from the one
+// three for B_FULLV, B_VFREE and B_DECAY (stage).  A parity can only be told from the one
 // before it, so whoever waits for a phase must stand between it and the next but one
 enum : uint32_t {
   B_FULLK = 0, B_FULLQ = 16, B_FULLV = 32, B_SC = 56, B_P = 72, B_VT = 88, B_DS = 104, B_DSFREE = 120, B_S = 136,
-  B_QS = 152, B_PV = 168, B_OFREE = 184, B_VFREE = 200, B_FIN = 224, B_TMEM = 240, B_ABORT = 244
+  B_QS = 152, B_PV = 168, B_OFREE = 184, B_VFREE = 200, B_DECAY = 224, B_FIN = 248, B_TMEM = 264
 };
 // of the state kernel: C_FULL and C_FREE one per stage
 enum : uint32_t {
-  C_FULL = 0, C_FREE = 24, C_VT = 48, C_DS = 64, C_DSFREE = 80, C_FIN = 96, C_TMEM = 104, C_ABORT = 108
+  C_FULL = 0, C_FREE = 24, C_VT = 48, C_DS = 64, C_DSFREE = 80, C_FIN = 96, C_TMEM = 104
 };
 
 // mbar_wait made short, its limit in polls instead of nanoseconds.  The roles of
-// a kernel run different code at the same time and wait at some twenty places;
+// a kernel run different code at the same time and wait at some thirty places;
 // where their loops together outgrow the SM's instruction cache, every warp
-// stalls on fetches (the main kernel's chunks took 2.1 us on the SMs nearest
-// their code and 3.3 us on the farthest).  A poll sleeps until the phase
-// completes or the hint runs out, so 2^15 of them are some seconds; polls that
-// return at once are still a millisecond, a hundred times the longest wait of a
-// running pipeline.
-__device__ __noinline__ void give_up(volatile int* abort_flag, unsigned int* status) {
-  *abort_flag = 1;
+// stalls on fetches.  A poll sleeps until the phase completes or the hint runs
+// out, so 2^15 of them are some seconds; polls that return at once are still a
+// millisecond, a hundred times the longest wait of a running pipeline.  Whoever
+// gives up says so and leaves; who waits for it runs out in turn.
+__device__ __noinline__ void give_up(unsigned int* status) {
   if (status) atomicOr(status, kStatusTimeoutBit);
 }
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const WaitCtl& w) {
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, unsigned int* status) {
   int polls = 32768;
 #pragma unroll 1
   while (!mbar_try_wait_suspend(bar, parity)) {
-    if (*w.abort_flag) return false;
     if (--polls == 0) {
-      give_up(w.abort_flag, w.status);
+      give_up(status);
       return false;
     }
   }
@@ -168,16 +171,35 @@ __device__ __forceinline__ float decay_out(const float (&a)[4], int w) {
   const float x = suffix_product(w == 0 ? a[0] : w == 1 ? a[1] : w == 2 ? a[2] : a[3]);
   return x * warp_product((w < 1 ? a[1] : 1.f) * (w < 2 ? a[2] : 1.f) * (w < 3 ? a[3] : 1.f));
 }
+// The same c_j from a chunk's shared decays.
+__device__ __forceinline__ float decay_to_end(const float* d, int w, int lane) {
+  float x = d[4 + 32 * w + lane];
+  if (w < 3) x *= d[3];
+  if (w < 2) x *= d[2];
+  if (w < 1) x *= d[1];
+  return x;
+}
 __device__ __forceinline__ float decay_chunk(const float (&a)[4]) {
   return warp_product(a[0] * a[1] * a[2] * a[3]);
 }
 
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
+// Two products in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
 // 32 bytes to global memory (32-byte aligned).
 __device__ __forceinline__ void st_global32(void* dst, const uint32_t* r) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(reinterpret_cast<uint64_t>(dst)), "r"(r[0]),
@@ -200,22 +222,23 @@ __device__ __forceinline__ void split8(const float* x, uint4& hi, uint4& lo) {
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// Row `row` of a 64-column tile scaled by f into the hi and lo tiles, in bf16
+// 16-byte pieces [c0, c1) of row `row` of a 64-column tile, scaled by f into the hi and lo tiles, in bf16
 // arithmetic: with f = f_hi + f_lo (bf16 each, 2^-17 left behind), hi = v f_hi
 // rounded, v f_hi - hi fits bf16 exactly (a product of two 8-bit significands
 // has 16 bits), and lo = that + v f_lo: three instructions for two values.
-__device__ __forceinline__ void scale_row(const uint8_t* tile, uint8_t* hi, uint8_t* lo, int row, float f) {
+__device__ __forceinline__ void scale_row(const uint8_t* tile, uint8_t* hi, uint8_t* lo, int row, float f, int c0,
+                                          int c1) {
   const uint32_t fh = pack2_bf16(f, f);
   const float rest = f - lo_half(fh);
   const uint32_t fl = pack2_bf16(rest, rest);
   constexpr uint32_t kNegZero = 0x80008000u;  // v f + (-0) = v f, its sign kept
 #pragma unroll 1
-  for (int c0 = 0; c0 < 8; c0 += 4) {
-    uint4 u[4];
+  for (; c0 < c1; c0 += 2) {
+    uint4 u[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const uint4*>(tile + sw128_off(row, c0 + i));
+    for (int i = 0; i < 2; ++i) u[i] = *reinterpret_cast<const uint4*>(tile + sw128_off(row, c0 + i));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
       uint32_t h[4], l[4];
 #pragma unroll
@@ -262,17 +285,19 @@ __device__ __forceinline__ void leave_state(float* dst, const float (&s)[NV]) {
     *reinterpret_cast<float4*>(dst + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
 }
 
-// s <- gamma s + this lane's increment
+// s <- gamma s + this lane's increment (its hi and lo halves at taddr, + 64)
 template <bool GATED>
 __device__ __forceinline__ void add_increment(float (&s)[NV], float gamma, uint32_t taddr) {
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
-    uint32_t x[16];
+    uint32_t x[16], y[16];
     tmem_ld16(taddr + 16 * h, x);
+    if (GATED) tmem_ld16(taddr + 64 + 16 * h, y);
     tmem_wait_ld();
 #pragma unroll
     for (int e = 0; e < 16; ++e)
-      s[16 * h + e] = GATED ? fmaf(gamma, s[16 * h + e], __uint_as_float(x[e])) : s[16 * h + e] + __uint_as_float(x[e]);
+      s[16 * h + e] = GATED ? fmaf(gamma, s[16 * h + e], __uint_as_float(x[e]) + __uint_as_float(y[e]))
+                            : s[16 * h + e] + __uint_as_float(x[e]);
   }
 }
 
@@ -293,22 +318,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int first = g * p.seg_chunks, n = min(p.seg_chunks, nch - first);  // chunks [first, first + n)
   const uint32_t bar = sb + L::BAR_OFF;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::BAR_OFF + B_TMEM);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::BAR_OFF + B_ABORT);
   const float* alpha = GATED ? p.alpha + (size_t)bh * T : nullptr;
 
   if (tid == 0) {
     for (uint32_t i = 0; i < 2; ++i) {
       for (uint32_t b : {B_FULLK, B_FULLQ, B_SC, B_DS, B_QS, B_PV}) mbar_init(bar + b + 8 * i, 1);
-      for (uint32_t b : {B_VT, B_DSFREE, B_S}) mbar_init(bar + b + 8 * i, 4);  // one arrival per warp
-      for (uint32_t b : {B_P, B_OFREE}) mbar_init(bar + b + 8 * i, 8);
+      for (uint32_t b : {B_DSFREE, B_S, B_OFREE}) mbar_init(bar + b + 8 * i, 4);  // one arrival per warp
+      for (uint32_t b : {B_P, B_VT}) mbar_init(bar + b + 8 * i, 8);
     }
     for (uint32_t i = 0; i < 3; ++i) {
       mbar_init(bar + B_FULLV + 8 * i, 1);
       mbar_init(bar + B_VFREE + 8 * i, 1);
+      mbar_init(bar + B_DECAY + 8 * i, 1);
     }
     mbar_init(bar + B_FIN, 1);
     mbar_init(bar + B_FIN + 8, 1);
-    *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == kWarpMma) {
@@ -319,11 +343,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = warp_uniform(*tmem_slot);
-  const WaitCtl wc{abort_flag, p.status, kWaitLimitNs};
+  unsigned int* const wc = p.status;
   const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
   auto done = [&](uint32_t b, int c) { return wait_bar(bar + b + 8 * (c & 1), (c >> 1) & 1, wc); };
   auto full_v = [&](int c) { return wait_bar(bar + B_FULLV + 8 * (c % 3), (c / 3) & 1, wc); };
   auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
+  // chunk c's decays: block products, then the rows'.  They take the place of
+  // chunk c-3's once the increment (c-2) and P (c-2) are there: the state has
+  // then added the increment (c-3), and O (c-4), which Q S (c-3) waited for, was
+  // drained by warps that had read their decays of chunk c-3 before
+  auto decays = [&](int c) { return reinterpret_cast<float*>(sm + L::SUF_OFF + (c % 3) * kDecayBytes); };
+  auto have_decays = [&](int c) {
+    return !GATED || wait_bar(bar + B_DECAY + 8 * (c % 3), (c / 3) & 1, wc);
+  };
   auto arrive = [&](uint32_t b, int c) {  // one arrival for the warp, after all its lanes
     __syncwarp();
     if (lane == 0) mbar_arrive(bar + b + 8 * (c & 1));
@@ -356,11 +388,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(sb + L::Q_OFF + (s * KB + kb) * kBlk, &tmQ, bar + B_FULLQ + 8 * s, kb * 64, row, bh);
         nq = c + 1;
       }
-      int zero = 0;  // never leave with copies in flight
-      const WaitCtl drain{&zero, p.status, kWaitLimitNs};
-      for (int c = nk > 2 ? nk - 2 : 0; c < nk; ++c) (void)wait_bar(bar + B_FULLK + 8 * (c & 1), (c >> 1) & 1, drain);
-      for (int c = nq > 2 ? nq - 2 : 0; c < nq; ++c) (void)wait_bar(bar + B_FULLQ + 8 * (c & 1), (c >> 1) & 1, drain);
-      for (int c = nv > 3 ? nv - 3 : 0; c < nv; ++c) (void)wait_bar(bar + B_FULLV + 8 * (c % 3), (c / 3) & 1, drain);
+      // never leave with copies in flight
+      for (int c = nk > 2 ? nk - 2 : 0; c < nk; ++c) (void)wait_bar(bar + B_FULLK + 8 * (c & 1), (c >> 1) & 1, wc);
+      for (int c = nq > 2 ? nq - 2 : 0; c < nq; ++c) (void)wait_bar(bar + B_FULLQ + 8 * (c & 1), (c >> 1) & 1, wc);
+      for (int c = nv > 3 ? nv - 3 : 0; c < nv; ++c) (void)wait_bar(bar + B_FULLV + 8 * (c % 3), (c / 3) & 1, wc);
     }
   } else if (warp == kWarpMma || warp == kWarpMma2) {
     // ------------------------------------------------------------------ MMA --
@@ -368,39 +399,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t id = idesc_bf16(128, 128, false, false);
       const uint32_t s = (c & 1) * KB * kBlk;
       const uint64_t dq = desc_k(sb + L::Q_OFF + s), dk = desc_k(sb + L::K_OFF + s);
-#pragma unroll
+#pragma unroll 2
       for (int ks = 0; ks < DK / 16; ++ks) {
         const uint32_t off = (ks >> 2) * kBlk + (ks & 3) * 32;
-        mma_bf16_ss_elect(tmem + TM_SC, desc_step(dq, off), desc_step(dk, off), id, ks > 0);
+        mma_bf16_ss_elect(tmem + TM_SC + 128 * (c & 1), desc_step(dq, off), desc_step(dk, off), id, ks > 0);
       }
       mma_commit_elect(bar + B_SC + 8 * (c & 1));
     };
-    // K^T hi + K^T lo (gated) or K^T V; with DK = 64 the product's upper 64 rows
+    // K^T [hi | lo] (gated) or K^T V; with DK = 64 the product's upper 64 rows
     // are computed from the next block and never read
     auto increment = [&](int c) {
-      constexpr uint32_t id = idesc_bf16(128, 64, true, true);
+      constexpr uint32_t id = idesc_bf16(128, GATED ? 128 : 64, true, true);
       const uint64_t da = desc_mn(sb + L::K_OFF + (c & 1) * KB * kBlk, kBlk);
       const uint64_t db = desc_mn(sb + (GATED ? L::VT_OFF : L::V_OFF + (c % 3) * kBlk), kBlk);
-#pragma unroll
-      for (int ks = 0; ks < (GATED ? 2 : 1) * C / 16; ++ks)
-        mma_bf16_ss_elect(tmem + TM_DS, desc_step(da, (ks & 7) * 2048), desc_step(db, ks * 2048), id, ks > 0);
+#pragma unroll 2
+      for (int ks = 0; ks < C / 16; ++ks)
+        mma_bf16_ss_elect(tmem + TM_DS, desc_step(da, ks * 2048), desc_step(db, ks * 2048), id, ks > 0);
       mma_commit_elect(bar + B_DS + 8 * (c & 1));
     };
     auto read_state = [&](int c) {
       constexpr uint32_t id = idesc_bf16(128, 64, false, true);
       const uint64_t dq = desc_k(sb + L::Q_OFF + (c & 1) * KB * kBlk), ds = desc_mn(sb + L::S_OFF, kBlk);
-#pragma unroll
+#pragma unroll 2
       for (int ks = 0; ks < DK / 16; ++ks)
-        mma_bf16_ss_elect(tmem + TM_QS + 64 * (c & 1), desc_step(dq, (ks >> 2) * kBlk + (ks & 3) * 32), desc_step(ds, ks * 2048), id,
+        mma_bf16_ss_elect(tmem + TM_QS, desc_step(dq, (ks >> 2) * kBlk + (ks & 3) * 32), desc_step(ds, ks * 2048), id,
                           ks > 0);
       mma_commit_elect(bar + B_QS + 8 * (c & 1));
     };
     auto inner = [&](int c) {
       constexpr uint32_t id = idesc_bf16(128, 64, false, true);
       const uint64_t dv = desc_mn(sb + L::V_OFF + (c % 3) * kBlk, kBlk);
-#pragma unroll
+#pragma unroll 2
       for (int ks = 0; ks < C / 16; ++ks)
-        mma_bf16_ts_elect(tmem + TM_PV, tmem + TM_P + 64 * (c & 1) + 8 * ks, desc_step(dv, ks * 2048), id, ks > 0);
+        mma_bf16_ts_elect(tmem + TM_PV, tmem + TM_SC + 128 * (c & 1) + 64 * (ks >> 2) + 8 * (ks & 3), desc_step(dv, ks * 2048), id, ks > 0);
       mma_commit_elect(bar + B_PV + 8 * (c & 1));
       mma_commit_elect(bar + B_VFREE + 8 * (c % 3));
     };
@@ -408,8 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWarpMma) {
       for (int c = 0; c <= n && ok; ++c) {
         if (c < n) {
-          // P (c-1) has been made of the scores that these overwrite
-          ok = all(done(B_FULLK, c) && done(B_FULLQ, c) && (c < 1 || done(B_P, c - 1)));
+          // P V (c-2) has read the P that these scores overwrite
+          ok = all(done(B_FULLK, c) && done(B_FULLQ, c) && (c < 2 || done(B_PV, c - 2)));
           if (!ok) break;
           tc_fence_after();
           scores(c);
@@ -427,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         increment(c);
-        ok = all(done(B_FULLQ, c) && done(B_S, c) && (c < 2 || done(B_OFREE, c - 2)));
+        ok = all(done(B_FULLQ, c) && done(B_S, c) && (c < 1 || done(B_OFREE, c - 1)));
         if (!ok) break;
         tc_fence_after();
         read_state(c);
@@ -436,122 +467,102 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();  // no MMA may outlive TMEM
     const uint32_t fin_bar = bar + B_FIN + (warp == kWarpMma ? 0 : 8);
     mma_commit_elect(fin_bar);
-    int zero = 0;
-    const WaitCtl fin{&zero, p.status, kWaitLimitNs};
-    (void)wait_bar(fin_bar, 0, fin);
-  } else if (warp >= kWarpO && warp < kWarpO + 8) {
-    // ----------------------------------------------------- scores, outputs --
-    const int half = (warp - kWarpO) >> 2, row = 32 * w + lane;
-    __nv_bfloat16* o_row = o_all + (size_t)bh * T * p.Dv + j0 + 32 * half;
-    float* suf = reinterpret_cast<float*>(sm + L::SUF_OFF);
-    float* blk = reinterpret_cast<float*>(sm + L::SUF_OFF + 1024);
-    float a = 1.f, pre = 1.f, into = 1.f, ahead = 1.f;
+    (void)wait_bar(fin_bar, 0, wc);
+  } else if (warp == kWarpDecay) {
+    // -------------------------------------------------------------- decays --
+    bool ok = true;
+    for (int c = 0; GATED && c < n && ok; ++c) {
+      ok = c < 2 || all(done(B_DS, c - 2) && done(B_P, c - 2));
+      if (!ok) break;
+      float* d = decays(c);
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        const int t = (first + c) * C + 32 * k + lane;
+        const float a = t < T ? __ldg(alpha + t) : 1.f, s = suffix_product(a);
+        d[4 + 32 * k + lane] = s;
+        if (lane == 0) d[k] = s * a;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar + B_DECAY + 8 * (c % 3));
+    }
+  } else if (warp >= kWarpP && warp < kWarpP + 8) {
+    // -------------------------------------------------------------- scores --
+    const int half = (warp - kWarpP) >> 2, row = 32 * w + lane;
+    float ahead = 1.f;
     auto load = [&](int c) {
       const int t = (first + c) * C + row;
       return GATED && c < n && t < T ? __ldg(alpha + t) : 1.f;
     };
-    auto factors = [&](int c) {  // chunk c's, into buffer c & 1
-      a = ahead;
-      ahead = load(c + 1);
-      pre = prefix_product(a);
-      if (half == 0) {
-        suf[(c & 1) * C + row] = suffix_product(a);
-        if (lane == 31) blk[(c & 1) * 4 + w] = pre;
-      }
-    };
     ahead = load(0);
-    if (GATED) factors(0);
     bool ok = true;
-    // the eight warps meet once a chunk, so one that gives up says so there
-    for (int c = 0; c <= n; ++c) {
-      const float into_before = into;
-      if (c < n) {
-        // every warp's factors are in place (and all have left the buffer of
-        // chunk c-1); P V (c-2) has read the P that this one overwrites
-        ok = named_bar_and(kBarO, 256, ok && done(B_SC, c) && (c < 2 || done(B_PV, c - 2)));
+    for (int c = 0; c < n && ok; ++c) {
+      const float a = ahead, pre = GATED ? prefix_product(a) : 1.f;
+      ahead = load(c + 1);
+      const float* bl = decays(c);
+      const float* sf = bl + 4;
+      if (GATED) {  // the increment (c-1) has read V~ (c-1)
+        ok = all(have_decays(c) && full_v(c) && (c < 1 || done(B_DS, c - 1)));
         if (!ok) break;
-        tc_fence_after();
-        const float* sf = suf + (c & 1) * C;
-        const float* bl = blk + (c & 1) * 4;
-        const uint32_t pt = lanes + TM_P + 64 * (c & 1);
-        float run = 1.f;
+        scale_row(sm + L::V_OFF + (c % 3) * kBlk, sm + L::VT_OFF, sm + L::VT_OFF + kBlk, row, decay_to_end(bl, w, lane),
+                  4 * half, 4 * half + 4);
+        fence_proxy_async_smem();
+        arrive(B_VT, c);
+      }
+      ok = all(done(B_SC, c));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t sc = lanes + TM_SC + 128 * (c & 1);
 #pragma unroll 1
-        for (int pc = 3; pc >= 0; --pc) {  // 16 columns at a time, the right ones first
-          const int c0 = 64 * half + 16 * pc, cb = c0 >> 5;
-          uint32_t d[8];
-          if (cb > w) {
+      for (int b = 0; b < 2; ++b) {
+        const int cb = 2 * half + b;
+        uint32_t d[16];
+        if (cb > w) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d[i] = 0;
-          } else {
-            uint32_t x[16];
-            float f[16];
-            tmem_ld16(lanes + TM_SC + c0, x);
-            if (GATED && cb < w) {
-              float mid = pre;
-              if (cb + 1 < w) mid *= bl[w - 1];
-              if (cb + 2 < w) mid *= bl[w - 2];
+          for (int i = 0; i < 16; ++i) d[i] = 0;
+        } else {
+          uint32_t x[32];
+          float2 f[16];
+          tmem_ld32(sc + 32 * cb, x);
+          if (GATED && cb < w) {
+            float mid = pre;
+            if (cb + 1 < w) mid *= bl[w - 1];
+            if (cb + 2 < w) mid *= bl[w - 2];
+            const float2 m2 = make_float2(mid, mid);
 #pragma unroll
-              for (int j = 0; j < 16; j += 4) {
-                const float4 u = *reinterpret_cast<const float4*>(sf + c0 + j);
-                f[j] = u.x * mid; f[j + 1] = u.y * mid; f[j + 2] = u.z * mid; f[j + 3] = u.w * mid;
-              }
-            } else if (GATED) {
-              const int b0 = c0 & 31;  // the block's first column of the piece
-#pragma unroll
-              for (int j = 15; j >= 0; --j) {  // run: the product of alpha over (column, row]
-                const float t = __shfl_sync(0xffffffffu, a, b0 + j + 1);
-                run = b0 + j < lane ? run * t : 1.f;
-                f[j] = run;
-              }
+            for (int j = 0; j < 16; j += 2) {
+              const float4 u = *reinterpret_cast<const float4*>(sf + 32 * cb + 2 * j);
+              f[j] = mul2(make_float2(u.x, u.y), m2);
+              f[j + 1] = mul2(make_float2(u.z, u.w), m2);
             }
-            tmem_wait_ld();
-            if (cb == w) {
-              const int top = lane - (c0 & 31);  // columns up to the diagonal
+          } else if (GATED) {  // the products of alpha over (column, row], zero right of the diagonal
+            float run = lane == 31 ? 1.f : 0.f;
+            f[15].y = run;
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (j > top) x[j] = 0;
+            for (int j = 30; j >= 0; --j) {
+              const float t = __shfl_sync(0xffffffffu, a, j + 1);
+              run = j == lane ? 1.f : run * t;
+              if (j & 1) f[j / 2].y = run;
+              else f[j / 2].x = run;
             }
-#pragma unroll
-            for (int j = 0; j < 16; j += 2)
-              d[j / 2] = GATED ? pack2_bf16(__uint_as_float(x[j]) * f[j], __uint_as_float(x[j + 1]) * f[j + 1])
-                               : pack2_bf16(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
           }
-          tmem_st8(pt + c0 / 2, d);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        arrive(B_P, c);
-        if (GATED) {
-          into = pre;
-          for (int u = 0; u < w; ++u) into *= bl[u];
-          if (c + 1 < n) factors(c + 1);
-        }
-      }
-      if (c >= 1) {
-        ok = all(ok && done(B_QS, c - 1) && done(B_PV, c - 1));
-        if (!ok) continue;
-        tc_fence_after();
-        const int t = (first + c - 1) * C + row;
-        uint32_t r[16];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t x[16], y[16];
-          tmem_ld16(lanes + TM_QS + 64 * ((c - 1) & 1) + 32 * half + 16 * h, x);
-          tmem_ld16(lanes + TM_PV + 32 * half + 16 * h, y);
           tmem_wait_ld();
+          if (!GATED && cb == w) {
 #pragma unroll
-          for (int e = 0; e < 16; e += 2)
-            r[8 * h + e / 2] = pack2_bf16(fmaf(into_before, __uint_as_float(x[e]), __uint_as_float(y[e])),
-                                          fmaf(into_before, __uint_as_float(x[e + 1]), __uint_as_float(y[e + 1])));
+            for (int j = 0; j < 32; ++j)
+              if (j > lane) x[j] = 0;
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float2 v = make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
+            if (GATED) v = mul2(v, f[j]);
+            d[j] = pack2_bf16(v.x, v.y);
+          }
         }
-        tc_fence_before();
-        arrive(B_OFREE, c - 1);
-        if (t < T) {
-          __nv_bfloat16* dst = o_row + (size_t)t * p.Dv;
-          st_global32(dst, r);
-          st_global32(dst + 16, r + 8);
-        }
+        tmem_st16(sc + 64 * half + 16 * b, d);  // over what this warp has read
       }
+      tmem_wait_st();
+      tc_fence_before();
+      arrive(B_P, c);
     }
   } else if (warp >= kWarpState && warp < kWarpState + 4) {
     // --------------------------------------------------------------- state --
@@ -570,16 +581,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     put();
     arrive(B_S, 0);
-    float a[4] = {1.f, 1.f, 1.f, 1.f};
-    if (GATED) load_alpha(alpha, T, first, a);
     bool ok = true;
     for (int c = 0; c < n && ok; ++c) {
-      const float gamma = GATED ? decay_chunk(a) : 1.f;
-      if (GATED && c + 1 < n) load_alpha(alpha, T, first + c + 1, a);
-      ok = all(done(B_DS, c));
+      ok = all(have_decays(c) && done(B_DS, c));
       if (!ok) break;
       tc_fence_after();
-      add_increment<GATED>(s, gamma, lanes + TM_DS);
+      const float* d = decays(c);
+      add_increment<GATED>(s, GATED ? d[0] * d[1] * d[2] * d[3] : 1.f, lanes + TM_DS);
       tc_fence_before();
       arrive(B_DSFREE, c);
       if (c + 1 < n) {
@@ -591,20 +599,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (ok && live && p.S_out && g == p.G - 1)
       leave_state(p.S_out + (size_t)bh * DK * p.Dv + (size_t)row * p.Dv + j0, s);
-  } else if (GATED && warp >= kWarpV) {
-    // --------------------------------------------------------- diag(c) V --
+  } else if (warp >= kWarpO) {
+    // ------------------------------------------------------------- outputs --
     const int row = 32 * w + lane;
-    float a[4];
-    load_alpha(alpha, T, first, a);
+    __nv_bfloat16* o_row = o_all + (size_t)bh * T * p.Dv + j0;
+    auto load = [&](int c) {
+      const int t = (first + c) * C + row;
+      return GATED && c < n && t < T ? __ldg(alpha + t) : 1.f;
+    };
+    float ahead = load(0), into = 1.f;
     bool ok = true;
-    for (int c = 0; c < n && ok; ++c) {
-      const float out = decay_out(a, w);
-      if (c + 1 < n) load_alpha(alpha, T, first + c + 1, a);
-      ok = all(full_v(c) && (c < 1 || done(B_DS, c - 1)));
-      if (!ok) break;
-      scale_row(sm + L::V_OFF + (c % 3) * kBlk, sm + L::VT_OFF, sm + L::VT_OFF + kBlk, row, out);
-      fence_proxy_async_smem();
-      arrive(B_VT, c);
+    for (int c = 0; c <= n && ok; ++c) {
+      const float into_before = into;
+      if (GATED && c < n) {
+        into = prefix_product(ahead);
+        ahead = load(c + 1);
+        ok = all(have_decays(c));
+        if (!ok) break;
+        const float* d = decays(c);
+        if (w > 0) into *= d[0];
+        if (w > 1) into *= d[1];
+        if (w > 2) into *= d[2];
+      }
+      if (c >= 1) {
+        ok = all(done(B_QS, c - 1) && done(B_PV, c - 1));
+        if (!ok) break;
+        tc_fence_after();
+        const int t = (first + c - 1) * C + row;
+        __nv_bfloat16* dst = o_row + (size_t)t * p.Dv;
+#pragma unroll 1
+        for (int h = 0; h < NV; h += 16) {
+          uint32_t x[16], y[16], r[8];
+          tmem_ld16(lanes + TM_QS + h, x);
+          tmem_ld16(lanes + TM_PV + h, y);
+          tmem_wait_ld();
+          if (h + 16 == NV) {
+            tc_fence_before();
+            arrive(B_OFREE, c - 1);
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e += 2)
+            r[e / 2] = pack2_bf16(fmaf(into_before, __uint_as_float(x[e]), __uint_as_float(y[e])),
+                                  fmaf(into_before, __uint_as_float(x[e + 1]), __uint_as_float(y[e + 1])));
+          if (t < T) st_global32(dst + h, r);
+        }
+      }
     }
   }
 
@@ -638,7 +677,6 @@ __global__ void __launch_bounds__(kStateThreads, 1)
   auto chunk = [&](int i) { return REV ? first + n - 1 - i : first + i; };
   const uint32_t bar = sb + L::BAR_OFF;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::BAR_OFF + C_TMEM);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::BAR_OFF + C_ABORT);
   const float* alpha = GATED ? p.alpha + (size_t)bh * T : nullptr;
 
   if (tid == 0) {
@@ -652,18 +690,17 @@ __global__ void __launch_bounds__(kStateThreads, 1)
       mbar_init(bar + C_DSFREE + 8 * i, 4);
     }
     mbar_init(bar + C_FIN, 1);
-    *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == kWarpMma) {
-    tmem_alloc(smem_u32(tmem_slot), 128);
+    tmem_alloc(smem_u32(tmem_slot), 256);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = warp_uniform(*tmem_slot);
-  const WaitCtl wc{abort_flag, p.status, kWaitLimitNs};
+  unsigned int* const wc = p.status;
   auto wait2 = [&](uint32_t b, int i) {  // a barrier pair by parity
     return __all_sync(0xffffffffu, wait_bar(bar + b + 8 * (i & 1), (i >> 1) & 1, wc)) != 0;
   };
@@ -684,10 +721,9 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         tma_load_3d(sb + L::Z_OFF + s * kBlk, &tmZ, f, j0, row, bh);
         issued = i + 1;
       }
-      int zero = 0;  // never leave with copies in flight
-      const WaitCtl drain{&zero, p.status, kWaitLimitNs};
+      // never leave with copies in flight
       for (int i = issued > NST ? issued - NST : 0; i < issued; ++i)
-        (void)wait_bar(bar + C_FULL + 8 * (i % NST), (i / NST) & 1, drain);
+        (void)wait_bar(bar + C_FULL + 8 * (i % NST), (i / NST) & 1, wc);
     }
   } else if (warp == kWarpMma) {
     bool ok = true;
@@ -697,20 +733,18 @@ __global__ void __launch_bounds__(kStateThreads, 1)
            (i < 2 || wait2(C_DSFREE, i - 2));
       if (!ok) break;
       tc_fence_after();
-      constexpr uint32_t id = idesc_bf16(128, 64, true, true);
+      constexpr uint32_t id = idesc_bf16(128, GATED ? 128 : 64, true, true);
       const uint64_t da = desc_mn(sb + L::X_OFF + s * KB * kBlk, kBlk);
       const uint64_t db = desc_mn(sb + (GATED ? L::VT_OFF : L::Z_OFF + s * kBlk), kBlk);
 #pragma unroll
-      for (int ks = 0; ks < (GATED ? 2 : 1) * C / 16; ++ks)
-        mma_bf16_ss_elect(tmem + 64 * b, desc_step(da, (ks & 7) * 2048), desc_step(db, ks * 2048), id, ks > 0);
+      for (int ks = 0; ks < C / 16; ++ks)
+        mma_bf16_ss_elect(tmem + 128 * b, desc_step(da, ks * 2048), desc_step(db, ks * 2048), id, ks > 0);
       mma_commit_elect(bar + C_DS + 8 * b);
       mma_commit_elect(bar + C_FREE + 8 * s);
     }
     tc_fence_after();  // no MMA may outlive TMEM
     mma_commit_elect(bar + C_FIN);
-    int zero = 0;
-    const WaitCtl fin{&zero, p.status, kWaitLimitNs};
-    (void)wait_bar(bar + C_FIN, 0, fin);
+    (void)wait_bar(bar + C_FIN, 0, wc);
   } else if (warp >= 4 && warp < 8) {
     const int row = 32 * w + lane;
     const bool live = row < DK, leader = warp == 4 && lane == 0;
@@ -760,7 +794,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
       ok = STORE ? named_bar_and(kBarS, 128, wait_bar(bar + C_DS + 8 * (i & 1), (i >> 1) & 1, wc)) : wait2(C_DS, i);
       if (!ok) break;
       tc_fence_after();
-      add_increment<GATED>(s, gamma, lanes + 64 * (i & 1));
+      add_increment<GATED>(s, gamma, lanes + 128 * (i & 1));
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar + C_DSFREE + 8 * (i & 1));
@@ -785,7 +819,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
       if (i + 1 < n) load_alpha(alpha, T, chunk(i + 1), a);
       ok = __all_sync(0xffffffffu, wait_stage(C_FULL, i)) && (i < 1 || wait2(C_DS, i - 1));
       if (!ok) break;
-      scale_row(sm + L::Z_OFF + (i % NST) * kBlk, sm + L::VT_OFF, sm + L::VT_OFF + kBlk, row, f);
+      scale_row(sm + L::Z_OFF + (i % NST) * kBlk, sm + L::VT_OFF, sm + L::VT_OFF + kBlk, row, f, 0, 8);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar + C_VT + 8 * (i & 1));
@@ -795,7 +829,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kWarpMma) tmem_dealloc(tmem, 128);
+  if (warp == kWarpMma) tmem_dealloc(tmem, 256);
 }
 
 // --------------------------------------------------------- gradient kernel --
@@ -821,7 +855,7 @@ constexpr int kGradThreads = 20 * 32, kGradPlain = 12 * 32, kBarE = 1, kBarT = 2
 enum : uint32_t {  // single-use mbarriers
   G_QK = 0, G_VO = 8, G_RH = 16, G_RL = 24, G_SH = 32, G_SL = 40, G_SC = 48, G_P = 56, G_DV = 64, G_XR = 72,
   G_DK = 80, G_DQ = 88, G_ACCFREE = 96, G_PAFREE = 104, G_RHREAD = 112, G_RLREAD = 120, G_DOTS = 128, G_FIN = 136,
-  G_TMEM = 144, G_ABORT = 148
+  G_TMEM = 144
 };
 template <int DK, int DV>
 struct GradLayout {
@@ -911,7 +945,6 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   const int nch = (T + C - 1) / C, bh = blockIdx.x / nch, c = blockIdx.x % nch, t0 = c * C;
   const uint32_t bar = sb + L::BAR_OFF;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::BAR_OFF + G_TMEM);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::BAR_OFF + G_ABORT);
   float* suf = reinterpret_cast<float*>(sm + L::SUF_OFF);
   float* blk = suf + C;
   float* thr = reinterpret_cast<float*>(sm + L::THR_OFF);
@@ -921,7 +954,6 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     for (uint32_t b : {G_QK, G_VO, G_RH, G_RL, G_SH, G_SL, G_SC, G_DV, G_XR, G_DK, G_DQ, G_PAFREE, G_FIN})
       mbar_init(bar + b, 1);
     for (uint32_t b : {G_P, G_ACCFREE, G_RHREAD, G_RLREAD, G_DOTS}) mbar_init(bar + b, 8);  // one arrival per warp
-    *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == kWarpMma) {
@@ -932,7 +964,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = warp_uniform(*tmem_slot);
-  const WaitCtl wc{abort_flag, status, kWaitLimitNs};
+  unsigned int* const wc = status;
   auto wait = [&](uint32_t b) { return wait_bar(bar + b, 0, wc); };
   auto wait_all = [&](uint32_t b) { return __all_sync(0xffffffffu, wait(b)) != 0; };
   auto arrive = [&](uint32_t b) {
@@ -977,9 +1009,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       } else {
         if (wait(G_XR)) state(G_SH, &tmS, L::X_OFF, at);
       }
-      int zero = 0;  // never leave with copies in flight
-      const WaitCtl drain{&zero, status, kWaitLimitNs};
-      for (int i = 0; i < n; ++i) (void)wait_bar(bar + got[i], 0, drain);
+      // never leave with copies in flight
+      for (int i = 0; i < n; ++i) (void)wait_bar(bar + got[i], 0, wc);
     }
   } else if (warp == kWarpMma) {
     // A: K-major tile of 64-column blocks `ab` apart; B: K-major blocks `bb` apart
@@ -1060,9 +1091,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     if (ok) mma_commit_elect(bar + G_DQ);
     tc_fence_after();  // no MMA may outlive TMEM
     mma_commit_elect(bar + G_FIN);
-    int zero = 0;
-    const WaitCtl fin{&zero, status, kWaitLimitNs};
-    (void)wait_bar(bar + G_FIN, 0, fin);
+    (void)wait_bar(bar + G_FIN, 0, wc);
   } else if (warp >= 4 && warp < 12) {
     // ----------------------------------------------------------- epilogues --
     const int row = 32 * w + lane, half = (warp - 4) >> 2;
@@ -1301,8 +1330,7 @@ cudaError_t launch_out(const GatedProblem& p, const GatedScan& s, cudaStream_t s
   constexpr int smem = (int)OutLayout<DK>::ALLOC;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  // without a gate the scaling warps have nothing to do
-  kern<<<(unsigned)((size_t)BH * s.G * (p.Dv / NV)), GATED ? kThreads : 32 * kWarpV, smem, st>>>(
+  kern<<<(unsigned)((size_t)BH * s.G * (p.Dv / NV)), kThreads, smem, st>>>(
       mq, mk, mv, static_cast<__nv_bfloat16*>(p.o), s);
   return cudaGetLastError();
 }
