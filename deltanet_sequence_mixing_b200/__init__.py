@@ -287,46 +287,89 @@ def deltanet_decode_step(q, k, v, beta, S, alpha=None, o=None, prestep: bool = F
     return o
 
 
-def _need_shape(t, name, shape, dtype, device):
-    """A contiguous tensor of this shape, type and device (None passes)."""
-    if t is not None:
-        _need(t, name, dtype, device)
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
+# The calls below serve single tokens too, where the host's time is the call's:
+# checks take one short path when nothing is wrong, addresses go to ctypes as
+# integers, and the device is switched only when it is another.
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+class _On:
+    """``with _On(device)``: make it current, where it is not already."""
+
+    __slots__ = ("to", "back")
+
+    def __init__(self, device):
+        self.to = device.index
+
+    def __enter__(self):
+        now = torch._C._cuda_getDevice()
+        self.back = None if now == self.to else now
+        if self.back is not None:
+            torch.cuda.set_device(self.to)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def _need_shape(t, name, shape, dtype, device, optional=False):
+    """A contiguous tensor of this shape, type and device (or None)."""
+    if t is None and optional:
+        return None
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.shape == shape
+            and t.is_contiguous()):
+        return t
+    _need(t, name, dtype, device)
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+_stream_workspaces: dict = {}
+_KEEP_BYTES = 32 << 20  # larger scratch is allocated for each call
 
 
 def _own_workspace(device, nbytes: int) -> torch.Tensor:
-    """The workspace of one call: the status word alone is shared (kernels only
-    ever set bits in it); scratch comes from the caching allocator for each
-    call, so calls on several streams and captured graphs never share it."""
-    if nbytes <= 256 and not torch.cuda.is_current_stream_capturing():
+    """The workspace of a call that brings none.  Without scratch it is the
+    device's cached status word (kernels only ever set bits in it).  Scratch is
+    kept for each stream, whose calls follow one another; under graph capture,
+    or where it is large, it comes from the caching allocator for this call
+    alone, so two graphs or two streams never share it."""
+    capturing = torch.cuda.is_current_stream_capturing()
+    if nbytes <= 256 and not capturing:
         return workspace_for(device)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    check("deltanet_workspace_init",
-          lib().deltanet_workspace_init(_ptr(ws), ws.numel(), _stream(device)))
+    stream = _raw_stream(device)
+    keep = nbytes <= _KEEP_BYTES and not capturing
+    ws = _stream_workspaces.get((device.index, stream)) if keep else None
+    if ws is None or ws.numel() < nbytes:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        check("deltanet_workspace_init", lib().deltanet_workspace_init(_at(ws), nbytes, stream))
+        if keep:
+            _stream_workspaces[(device.index, stream)] = ws
     return ws
 
 
 def _recurrence_inputs(q, k, v, alpha, rank):
-    """Sizes of a gated recurrence call, its inputs checked."""
+    """Device, type and sizes of a gated recurrence call, its inputs checked."""
     _need(q, "q")
     dev, dtype = q.device, q.dtype
     if dtype not in _DT:
         raise TypeError(f"unsupported dtype {dtype}")
-    if q.dim() != rank:
-        raise ValueError(f"q must have {rank} dimensions, got {q.dim()}")
-    lead, Dk = q.shape[:-1], q.shape[-1]
-    _need(v, "v", dtype, dev)
+    shape = q.shape
+    if len(shape) != rank:
+        raise ValueError(f"q must have {rank} dimensions, got {len(shape)}")
+    _need_shape(k, "k", shape, dtype, dev)
+    if not isinstance(v, torch.Tensor):
+        raise TypeError("v must be a torch.Tensor")
     if v.dim() != rank:
         raise ValueError(f"v must have {rank} dimensions, got {v.dim()}")
-    Dv = v.shape[-1]
-    _need_shape(k, "k", q.shape, dtype, dev)
-    if k is None:
-        raise TypeError("k must be a torch.Tensor")
+    lead, Dv = shape[:-1], v.shape[-1]
     _need_shape(v, "v", (*lead, Dv), dtype, dev)
-    _need_shape(alpha, "alpha", lead, torch.float32, dev)
-    return dev, dtype, lead, Dk, Dv
+    _need_shape(alpha, "alpha", lead, torch.float32, dev, True)
+    return dev, dtype, lead, shape[-1], Dv
 
 
 def _gated_bytes(fn, B, H, T, Dk, Dv, dtype):
@@ -342,21 +385,21 @@ def gated_linear_attn_fwd(q, k, v, alpha=None, S0=None, o=None, S_out=None, work
     or None (1); S0: (B,H,Dk,Dv) f32 or None (0).  S_out may be S0.  Returns
     (o, S_out): (B,H,T,Dv) of q's type and (B,H,Dk,Dv) f32."""
     dev, dtype, (B, H, T), Dk, Dv = _recurrence_inputs(q, k, v, alpha, 4)
-    _need_shape(S0, "S0", (B, H, Dk, Dv), torch.float32, dev)
-    with torch.cuda.device(dev):
+    _need_shape(S0, "S0", (B, H, Dk, Dv), torch.float32, dev, True)
+    _need_shape(o, "o", (B, H, T, Dv), dtype, dev, True)
+    _need_shape(S_out, "S_out", (B, H, Dk, Dv), torch.float32, dev, True)
+    with _On(dev):
         if o is None:
-            o = torch.empty(B, H, T, Dv, dtype=dtype, device=dev)
+            o = torch.empty_like(v)
         if S_out is None:
             S_out = torch.empty(B, H, Dk, Dv, dtype=torch.float32, device=dev)
-        _need_shape(o, "o", (B, H, T, Dv), dtype, dev)
-        _need_shape(S_out, "S_out", (B, H, Dk, Dv), torch.float32, dev)
-        ws = workspace
-        if ws is None:
+        if workspace is None:
             ws = _own_workspace(dev, _gated_bytes("gated_linear_attn_workspace_bytes", B, H, T, Dk, Dv, dtype))
-        _need(ws, "workspace", torch.uint8, dev)
+        else:
+            ws = _need(workspace, "workspace", torch.uint8, dev)
         check("gated_linear_attn_fwd", lib().gated_linear_attn_fwd(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(S0), _ptr(o), _ptr(S_out),
-            B, H, T, Dk, Dv, _DT[dtype], _ptr(ws), ws.numel(), _stream(dev)))
+            _at(q), _at(k), _at(v), _at(alpha), _at(S0), _at(o), _at(S_out),
+            B, H, T, Dk, Dv, _DT[dtype], _at(ws), ws.numel(), _raw_stream(dev)))
     return o, S_out
 
 
@@ -365,24 +408,22 @@ def gated_linear_attn_bwd(q, k, v, dO, alpha=None, S0=None, dS_T=None, workspace
     Returns dict(dq, dk, dv, dlog_alpha, dS0): dq, dk, dv of q's type (summed in
     float32, rounded once), dlog_alpha (None when ungated) and dS0 float32."""
     dev, dtype, (B, H, T), Dk, Dv = _recurrence_inputs(q, k, v, alpha, 4)
-    if dO is None:
-        raise TypeError("dO must be a torch.Tensor")
     _need_shape(dO, "dO", (B, H, T, Dv), dtype, dev)
     for t, n in ((S0, "S0"), (dS_T, "dS_T")):
-        _need_shape(t, n, (B, H, Dk, Dv), torch.float32, dev)
-    with torch.cuda.device(dev):
+        _need_shape(t, n, (B, H, Dk, Dv), torch.float32, dev, True)
+    with _On(dev):
         f = dict(dtype=torch.float32, device=dev)
         out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
                    dlog_alpha=None if alpha is None else torch.empty(B, H, T, **f),
                    dS0=torch.empty(B, H, Dk, Dv, **f))
-        ws = workspace
-        if ws is None:
+        if workspace is None:
             ws = _own_workspace(dev, _gated_bytes("gated_linear_attn_bwd_workspace_bytes", B, H, T, Dk, Dv, dtype))
-        _need(ws, "workspace", torch.uint8, dev)
+        else:
+            ws = _need(workspace, "workspace", torch.uint8, dev)
         check("gated_linear_attn_bwd", lib().gated_linear_attn_bwd(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(S0), _ptr(dO), _ptr(dS_T), _ptr(out["dq"]),
-            _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dlog_alpha"]), _ptr(out["dS0"]),
-            B, H, T, Dk, Dv, _DT[dtype], _ptr(ws), ws.numel(), _stream(dev)))
+            _at(q), _at(k), _at(v), _at(alpha), _at(S0), _at(dO), _at(dS_T), _at(out["dq"]),
+            _at(out["dk"]), _at(out["dv"]), _at(out["dlog_alpha"]), _at(out["dS0"]),
+            B, H, T, Dk, Dv, _DT[dtype], _at(ws), ws.numel(), _raw_stream(dev)))
     return out
 
 
@@ -391,15 +432,13 @@ def gated_linear_attn_decode_step(q, k, v, S, alpha=None, o=None):
     (B,H,Dk); v: (B,H,Dv); alpha: (B,H) f32 or None; S: (B,H,Dk,Dv) f32, updated
     in place.  Returns o (B,H,Dv) of q's type."""
     dev, dtype, (B, H), Dk, Dv = _recurrence_inputs(q, k, v, alpha, 3)
-    if S is None:
-        raise TypeError("S must be a torch.Tensor")
     _need_shape(S, "S", (B, H, Dk, Dv), torch.float32, dev)
-    with torch.cuda.device(dev):
+    _need_shape(o, "o", (B, H, Dv), dtype, dev, True)
+    with _On(dev):
         if o is None:
-            o = torch.empty(B, H, Dv, dtype=dtype, device=dev)
-        _need_shape(o, "o", (B, H, Dv), dtype, dev)
+            o = torch.empty_like(v)
         check("gated_linear_attn_decode_step", lib().gated_linear_attn_decode_step(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(S), _ptr(o), B, H, Dk, Dv, _DT[dtype], _stream(dev)))
+            _at(q), _at(k), _at(v), _at(alpha), _at(S), _at(o), B, H, Dk, Dv, _DT[dtype], _raw_stream(dev)))
     return o
 
 
@@ -436,7 +475,7 @@ def _qk_args(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, silu, int
     if k.shape != (B, T, Hk, D):
         raise ValueError(f"k must have shape {(B, T, 'Hk', D)}, got {tuple(k.shape)}")
     for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        _need_shape(t, n, (D,), torch.float32, dev)
+        _need_shape(t, n, (D,), torch.float32, dev, True)
     pos_stride = 0
     if positions is not None:
         _need(positions, "positions", torch.int64, dev)
@@ -471,17 +510,17 @@ def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, positions=None, inv_fre
     (B,Hq,T,D) and (B,Hk,T,D), contiguous: what the mixing calls take."""
     dev, dtype, B, T, Hq, Hk, D, rot, ps, eps, opts = _qk_args(
         q, k, q_weight, k_weight, positions, inv_freq, norm, eps, silu, interleaved)
-    with torch.cuda.device(dev):
+    _need_shape(q_out, "q_out", (B, Hq, T, D), dtype, dev, True)
+    _need_shape(k_out, "k_out", (B, Hk, T, D), dtype, dev, True)
+    with _On(dev):
         if q_out is None:
             q_out = torch.empty(B, Hq, T, D, dtype=dtype, device=dev)
         if k_out is None:
             k_out = torch.empty(B, Hk, T, D, dtype=dtype, device=dev)
-        _need_shape(q_out, "q_out", (B, Hq, T, D), dtype, dev)
-        _need_shape(k_out, "k_out", (B, Hk, T, D), dtype, dev)
         check("qk_norm_rope_fwd", lib().qk_norm_rope_fwd(
-            _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), _ptr(q_out),
-            _ptr(k_out), B, T, Hq, Hk, D, rot, *_row_strides(q), *_row_strides(k), ps, eps, opts, _DT[dtype],
-            _stream(dev)))
+            _at(q), _at(k), _at(q_weight), _at(k_weight), _at(positions), _at(inv_freq), _at(q_out),
+            _at(k_out), B, T, Hq, Hk, D, rot, *_row_strides(q), *_row_strides(k), ps, eps, opts, _DT[dtype],
+            _raw_stream(dev)))
     return q_out, k_out
 
 
@@ -502,7 +541,7 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, positio
         raise TypeError(f"dq_out must be {dtype} or torch.float32, got {gdt}")
     _need_shape(dq_out, "dq_out", (B, Hq, T, D), gdt, dev)
     _need_shape(dk_out, "dk_out", (B, Hk, T, D), gdt, dev)
-    with torch.cuda.device(dev):
+    with _On(dev):
         if dq is None:
             dq = torch.empty(B, T, Hq, D, dtype=dtype, device=dev)
         if dk is None:
@@ -521,19 +560,25 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, positio
         if ws is not None:
             _need(ws, "workspace", torch.uint8, dev)
         check("qk_norm_rope_bwd", lib().qk_norm_rope_bwd(
-            _ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
-            _ptr(inv_freq), _ptr(dq), _ptr(dk), _ptr(dw[0]), _ptr(dw[1]), B, T, Hq, Hk, D, rot,
+            _at(q), _at(k), _at(dq_out), _at(dk_out), _at(q_weight), _at(k_weight), _at(positions),
+            _at(inv_freq), _at(dq), _at(dk), _at(dw[0]), _at(dw[1]), B, T, Hq, Hk, D, rot,
             *_row_strides(q), *_row_strides(k), *_row_strides(dq), *_row_strides(dk), ps, eps, opts, _DT[dtype],
-            _DT[gdt], _ptr(ws), 0 if ws is None else ws.numel(), _stream(dev)))
+            _DT[gdt], _at(ws), 0 if ws is None else ws.numel(), _raw_stream(dev)))
     return dict(dq=dq, dk=dk, dq_weight=dw[0], dk_weight=dw[1])
 
 
 def deltanet_get_device_status(device=None, workspace=None) -> int:
     """Synchronise and return the sticky device status of ``workspace`` (or of the
-    cached workspace of ``device``)."""
+    cached workspaces of ``device``: the first that is not DN_OK)."""
     device = torch.device(device if device is not None else "cuda")
     ws = workspace if workspace is not None else workspace_for(device)
-    return lib().deltanet_get_device_status(_ptr(ws), _stream(device))
+    status = lib().deltanet_get_device_status(_ptr(ws), _stream(device))
+    if workspace is None and status == 0 and _stream_workspaces:
+        index = torch.cuda.current_device() if device.index is None else device.index
+        for (i, stream), kept in list(_stream_workspaces.items()):
+            if i == index and status == 0:
+                status = lib().deltanet_get_device_status(_ptr(kept), stream)
+    return status
 
 
 def deltanet_selftest_wait_timeout(wait_ns: int, workspace, device=None) -> int:
