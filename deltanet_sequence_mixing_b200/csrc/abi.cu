@@ -352,11 +352,11 @@ int validate_gated_sizes(int B, int H, int T, int Dk, int Dv, int dt) {
   if (dt != DN_F32 && dt != DN_BF16) return DN_ERR_UNSUPPORTED;
   if (B < 0 || H < 0 || T < 0) return DN_ERR_INVALID_ARG;
   if (!valid_dim(Dk) || !valid_dim(Dv)) return DN_ERR_UNSUPPORTED;
-  // one CTA per (b, h, 32-column slice of Dv) or per (b, h, chunk) on a
+  // one CTA per (b, h, chunk, 32-column slice of Dv) at most, on a
   // one-dimensional grid
   const long long BH = (long long)B * H;
   if (BH > INT_MAX / 4) return DN_ERR_UNSUPPORTED;
-  if (BH * (((long long)T + dn::kGatedSimtChunk - 1) / dn::kGatedSimtChunk) > INT_MAX) return DN_ERR_UNSUPPORTED;
+  if (BH * (((long long)T + dn::kGatedSimtChunk - 1) / dn::kGatedSimtChunk) > INT_MAX / 4) return DN_ERR_UNSUPPORTED;
   return DN_OK;
 }
 
@@ -444,7 +444,10 @@ extern "C" {
 
 size_t gated_linear_attn_workspace_bytes(int B, int H, int T, int Dk, int Dv, dn_dtype dt) {
   if (validate_gated_sizes(B, H, T, Dk, Dv, dt) != DN_OK) return 0;
-  if (dt == DN_F32 || (long long)B * H == 0 || T == 0) return kStatusBytes;
+  if ((long long)B * H == 0 || T == 0) return kStatusBytes;
+  if (dt == DN_F32)
+    return kStatusBytes +
+           (dn::gated_simt_walks(B * H, T, Dv, sm_count_now()) ? 0 : dn::gated_simt_bytes(B * H, T, Dk, Dv, 1));
   int G, per;
   gated_split(B, H, T, Dv, &G, &per);
   return kStatusBytes + dn::gated_segment_bytes(B * H, G, Dk, Dv);
@@ -477,7 +480,10 @@ int gated_linear_attn_fwd(const void* q, const void* k, const void* v, const flo
   p.bf16 = dt == DN_BF16;
   p.status = static_cast<unsigned int*>(workspace);
   p.scratch = static_cast<uint8_t*>(workspace) + kStatusBytes;
-  if (!p.bf16) return map_cuda(dn::launch_gated_simt_fwd(p, st));
+  if (!p.bf16) {
+    if (dn::gated_simt_walks(B * H, T, Dv, sm_count_now())) p.scratch = nullptr;
+    return map_cuda(dn::launch_gated_simt_fwd(p, st));
+  }
   gated_split(B, H, T, Dv, &p.G, &p.seg_chunks);
   return map_cuda(dn::launch_gated_tc_fwd(p, st));
 }
@@ -490,8 +496,7 @@ size_t gated_linear_attn_bwd_workspace_bytes(int B, int H, int T, int Dk, int Dv
     gated_split(B, H, T, Dv, &G, &per);
     return kStatusBytes + dn::gated_bwd_bytes(B * H, T, G, Dk, Dv);
   }
-  const size_t chunks = ((size_t)T + dn::kGatedSimtChunk - 1) / dn::kGatedSimtChunk;
-  return kStatusBytes + 2 * (size_t)B * H * chunks * Dk * Dv * 4;
+  return kStatusBytes + dn::gated_simt_bytes(B * H, T, Dk, Dv, 2);
 }
 
 int gated_linear_attn_bwd(const void* q, const void* k, const void* v, const float* alpha, const float* S0,

@@ -21,10 +21,13 @@
 // where the first term is the suffix sum of (row sum - column sum) of M below
 // its diagonal.  Sums stay inside one chunk, so no error travels along T.
 //
-// Three kernels: the state scan (forward, or reverse with (q, dO) in the place
-// of (k, v); one CTA per (b, h, 32 columns of Dv), serial over chunks), which
-// stores each chunk's entry state when the gradient needs it, and the gradient
-// of every chunk side by side.
+// Kernels: every chunk's own increment of the state, side by side (`local`); the
+// states between them, one multiply-add per chunk and element (`between`);
+// outputs or gradients of every chunk, side by side (`out`, `grad`).  The
+// gradient takes the first two forward with (k, v) and from the end with
+// (q, dO).  With heads enough to fill the GPU the forward instead walks the
+// chunks of each head (`out` without stored states): the same products without
+// the states' way through memory.
 #include "kernels.h"
 
 namespace dn {
@@ -82,113 +85,172 @@ __device__ __forceinline__ float chunk_decays(const float* alpha, int n, float* 
   return __shfl_sync(0xffffffffu, pre, 31);
 }
 
-// ------------------------------------------------------------------- scan --
-// Forward: x = k, z = v, S <- gamma S + K^T diag(c) V, and o if OUT.
-// Reverse: x = q, z = dO, chunks from the last, R <- gamma R + Q^T diag(G) dO.
-// `states` (if not null) takes the state that each chunk is entered with, in
-// the scan's own direction.
-template <int DK, bool REV, bool OUT>
-__global__ void __launch_bounds__(kThreads) gated_simt_scan_kernel(const GatedProblem p, float* states) {
+// ----------------------------------------------------------------- states --
+// One CTA per (b, h, chunk) and direction (blockIdx.y: 0 forward, 1 from the
+// end): the chunk's increment X^T diag(f) Z of the state, and gamma.
+template <int DK, int DV>
+__global__ void __launch_bounds__(kThreads) gated_simt_local_kernel(const GatedProblem p, float* S, float* R,
+                                                                    float* gammas) {
+  constexpr int KP = DK + 1, VP = DV + 1, RK = DK / 16, RV = DV / 16;
+  __shared__ float into[C], out[C];
+  extern __shared__ float sm[];
+  float* Xs = sm;           // C x KP
+  float* Zs = Xs + C * KP;  // C x VP
+  const int tid = threadIdx.x, r0 = tid >> 4, c0 = tid & 15;
+  const int T = p.T, nch = (T + C - 1) / C;
+  const size_t bh = blockIdx.x / nch;
+  const int c = (int)(blockIdx.x % nch), t0 = c * C, n = min(C, T - t0);
+  const bool rev = blockIdx.y;
+  const float* x = static_cast<const float*>(rev ? p.q : p.k) + (bh * T + t0) * DK;
+  const float* z = static_cast<const float*>(rev ? p.dO : p.v) + (bh * T + t0) * DV;
+  for (int i = tid; i < C * DK; i += kThreads) Xs[(i / DK) * KP + i % DK] = i / DK < n ? x[i] : 0.f;
+  for (int i = tid; i < C * DV; i += kThreads) Zs[(i / DV) * VP + i % DV] = i / DV < n ? z[i] : 0.f;
+  if (tid < 32) {
+    const float g = chunk_decays(p.alpha ? p.alpha + bh * T + t0 : nullptr, n, into, out, nullptr);
+    if (tid == 0 && !rev) gammas[blockIdx.x] = g;
+  }
+  __syncthreads();
+  for (int i = tid; i < C * DK; i += kThreads) Xs[(i / DK) * KP + i % DK] *= rev ? into[i / DK] : out[i / DK];
+  __syncthreads();
+  float a[RK][RV] = {};
+  product<RK, RV>(C, Xs, 1, KP, Zs, VP, 1, a);
+  float* dst = (rev ? R : S) + (size_t)blockIdx.x * DK * DV;
+#pragma unroll
+  for (int xx = 0; xx < RK; ++xx)
+#pragma unroll
+    for (int y = 0; y < RV; ++y) dst[(r0 + 16 * xx) * DV + c0 + 16 * y] = a[xx][y];
+}
+
+// Four elements of the state per thread, over the chunks of their (b, h): each
+// chunk's increment becomes the state that the chunk is entered with, in the
+// scan's direction.
+__global__ void __launch_bounds__(kThreads) gated_simt_between_kernel(const GatedProblem p, float* S, float* R,
+                                                                      const float* gammas) {
+  const int nch = (p.T + C - 1) / C, elems = p.Dk * p.Dv, quads = elems / 4;
+  const size_t at = (size_t)blockIdx.x * kThreads + threadIdx.x, bh = at / quads;  // quads is a multiple of kThreads
+  const bool rev = blockIdx.y;
+  const float* S_in = rev ? p.dS_T : p.S0;
+  float* S_end = rev ? p.dS0 : p.S_out;
+  float4* st = reinterpret_cast<float4*>((rev ? R : S) + bh * nch * elems) + at % quads;
+  const float* g = gammas + bh * nch;
+  float4 s = S_in ? reinterpret_cast<const float4*>(S_in + bh * elems)[at % quads] : make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int AHEAD = 8;
+  for (int c0 = 0; c0 < nch; c0 += AHEAD) {
+    float4 d[AHEAD];
+    float gam[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int cc = c0 + i, c = rev ? nch - 1 - cc : cc;
+      if (cc < nch) {
+        d[i] = st[(size_t)c * quads];
+        gam[i] = g[c];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int cc = c0 + i, c = rev ? nch - 1 - cc : cc;
+      if (cc < nch) {
+        st[(size_t)c * quads] = s;
+        s = make_float4(fmaf(gam[i], s.x, d[i].x), fmaf(gam[i], s.y, d[i].y), fmaf(gam[i], s.z, d[i].z),
+                        fmaf(gam[i], s.w, d[i].w));
+      }
+    }
+  }
+  if (S_end) reinterpret_cast<float4*>(S_end + bh * elems)[at % quads] = s;
+}
+
+// ----------------------------------------------------------------- outputs --
+// One CTA per (b, h, 32 columns of Dv) over all chunks, or with PAR per chunk
+// too, from the stored states.
+template <int DK, bool PAR>
+__global__ void __launch_bounds__(kThreads) gated_simt_out_kernel(const GatedProblem p, const float* states) {
   constexpr int KP = DK + 1, VP = NV + 1, RK = DK / 16;
   __shared__ float into[C], out[C], gam;
   extern __shared__ float sm[];
-  float* Xs = sm;               // C x KP: k (forward), q (reverse)
-  float* Zs = Xs + C * KP;      // C x VP: v (forward), dO (reverse)
-  float* Ss = Zs + C * VP;      // DK x VP
-  float* Qs = Ss + DK * VP;     // C x KP (OUT)
-  float* Ps = Qs + C * KP;      // C x CP (OUT)
-  float* Ds = Ps + C * CP;      // C x CP (OUT)
+  float* Ks = sm;               // C x KP
+  float* Vs = Ks + C * KP;      // C x VP
+  float* Ss = Vs + C * VP;      // DK x VP
+  float* Qs = Ss + DK * VP;     // C x KP
+  float* Ps = Qs + C * KP;      // C x CP
+  float* Ds = Ps + C * CP;      // C x CP
   const int tid = threadIdx.x, r0 = tid >> 4, c0 = tid & 15;
-  const int T = p.T, Dv = p.Dv, nch = (T + C - 1) / C, nsl = Dv / NV;
-  const size_t bh = blockIdx.x / nsl;
-  const int j0 = (int)(blockIdx.x % nsl) * NV;
+  const int T = p.T, Dv = p.Dv, nch = (T + C - 1) / C, nsl = Dv / NV, per = PAR ? nch : 1;
+  const size_t bh = blockIdx.x / nsl / per;
+  const int j0 = (int)(blockIdx.x % nsl) * NV, only = (int)(blockIdx.x / nsl % per);
   const size_t sblk = (size_t)DK * Dv;
-  const float* x = static_cast<const float*>(REV ? p.q : p.k) + bh * T * DK;
+  const float* k = static_cast<const float*>(p.k) + bh * T * DK;
   const float* q = static_cast<const float*>(p.q) + bh * T * DK;
-  const float* z = static_cast<const float*>(REV ? p.dO : p.v) + bh * T * Dv + j0;
-  float* o = OUT ? static_cast<float*>(p.o) + bh * T * Dv + j0 : nullptr;
+  const float* v = static_cast<const float*>(p.v) + bh * T * Dv + j0;
+  float* o = static_cast<float*>(p.o) + bh * T * Dv + j0;
   const float* alpha = p.alpha ? p.alpha + bh * T : nullptr;
-  const float* S_in = REV ? p.dS_T : p.S0;
-  float* S_end = REV ? p.dS0 : p.S_out;
+  const float* S_in = PAR ? states + (bh * nch + only) * sblk : p.S0 ? p.S0 + bh * sblk : nullptr;
 
   float s[RK][2];  // this thread's rows r0 + 16 x, columns c0 + 16 y of the state
 #pragma unroll
   for (int xx = 0; xx < RK; ++xx)
 #pragma unroll
-    for (int y = 0; y < 2; ++y)
-      s[xx][y] = S_in ? S_in[bh * sblk + (size_t)(r0 + 16 * xx) * Dv + j0 + c0 + 16 * y] : 0.f;
+    for (int y = 0; y < 2; ++y) s[xx][y] = S_in ? S_in[(size_t)(r0 + 16 * xx) * Dv + j0 + c0 + 16 * y] : 0.f;
 
-  for (int cc = 0; cc < nch; ++cc) {
-    const int c = REV ? nch - 1 - cc : cc, t0 = c * C, n = min(C, T - t0);
+  for (int c = only; c < (PAR ? only + 1 : nch); ++c) {
+    const int t0 = c * C, n = min(C, T - t0);
     __syncthreads();  // the products of the chunk before have read the tiles
     for (int i = tid; i < C * DK; i += kThreads) {
       const int r = i / DK, d = i % DK;
-      Xs[r * KP + d] = r < n ? x[(size_t)(t0 + r) * DK + d] : 0.f;
-      if (OUT) Qs[r * KP + d] = r < n ? q[(size_t)(t0 + r) * DK + d] : 0.f;
+      Ks[r * KP + d] = r < n ? k[(size_t)(t0 + r) * DK + d] : 0.f;
+      Qs[r * KP + d] = r < n ? q[(size_t)(t0 + r) * DK + d] : 0.f;
     }
     for (int i = tid; i < C * NV; i += kThreads) {
       const int r = i / NV, d = i % NV;
-      Zs[r * VP + d] = r < n ? z[(size_t)(t0 + r) * Dv + d] : 0.f;
+      Vs[r * VP + d] = r < n ? v[(size_t)(t0 + r) * Dv + d] : 0.f;
     }
     if (tid < 32) {
-      const float g = chunk_decays(alpha ? alpha + t0 : nullptr, n, into, out, OUT ? Ds : nullptr);
+      const float g = chunk_decays(alpha ? alpha + t0 : nullptr, n, into, out, Ds);
       if (tid == 0) gam = g;
     }
 #pragma unroll
     for (int xx = 0; xx < RK; ++xx)
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        if (OUT) Ss[(r0 + 16 * xx) * VP + c0 + 16 * y] = s[xx][y];
-        if (states) states[(bh * nch + c) * sblk + (size_t)(r0 + 16 * xx) * Dv + j0 + c0 + 16 * y] = s[xx][y];
-      }
+      for (int y = 0; y < 2; ++y) Ss[(r0 + 16 * xx) * VP + c0 + 16 * y] = s[xx][y];
     __syncthreads();
-    if (OUT) {
-      float a[2][2] = {};
-      product<2, 2>(DK, Qs, KP, 1, Xs, 1, KP, a);
+    float a[2][2] = {};
+    product<2, 2>(DK, Qs, KP, 1, Ks, 1, KP, a);
 #pragma unroll
-      for (int xx = 0; xx < 2; ++xx)
+    for (int xx = 0; xx < 2; ++xx)
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const int i = r0 + 16 * xx, j = c0 + 16 * y;
-          Ps[i * CP + j] = j <= i ? a[xx][y] * Ds[i * CP + j] : 0.f;
-        }
-      float qs[2][2] = {};
-      product<2, 2>(DK, Qs, KP, 1, Ss, VP, 1, qs);
-      __syncthreads();
+      for (int y = 0; y < 2; ++y) {
+        const int i = r0 + 16 * xx, j = c0 + 16 * y;
+        Ps[i * CP + j] = j <= i ? a[xx][y] * Ds[i * CP + j] : 0.f;
+      }
+    float qs[2][2] = {};
+    product<2, 2>(DK, Qs, KP, 1, Ss, VP, 1, qs);
+    __syncthreads();
 #pragma unroll
-      for (int xx = 0; xx < 2; ++xx)
+    for (int xx = 0; xx < 2; ++xx)
 #pragma unroll
-        for (int y = 0; y < 2; ++y) qs[xx][y] *= into[r0 + 16 * xx];
-      product<2, 2>(C, Ps, CP, 1, Zs, VP, 1, qs);
+      for (int y = 0; y < 2; ++y) qs[xx][y] *= into[r0 + 16 * xx];
+    product<2, 2>(C, Ps, CP, 1, Vs, VP, 1, qs);
 #pragma unroll
-      for (int xx = 0; xx < 2; ++xx)
+    for (int xx = 0; xx < 2; ++xx)
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
-          if (r0 + 16 * xx < n) o[(size_t)(t0 + r0 + 16 * xx) * Dv + c0 + 16 * y] = qs[xx][y];
-      __syncthreads();  // P V has read Zs
-    }
-    for (int i = tid; i < C * NV; i += kThreads) {
-      const int r = i / NV;
-      Zs[r * VP + i % NV] *= REV ? into[r] : out[r];
-    }
+      for (int y = 0; y < 2; ++y)
+        if (r0 + 16 * xx < n) o[(size_t)(t0 + r0 + 16 * xx) * Dv + c0 + 16 * y] = qs[xx][y];
+    if (PAR) break;
+    __syncthreads();  // P V has read Vs
+    for (int i = tid; i < C * NV; i += kThreads) Vs[(i / NV) * VP + i % NV] *= out[i / NV];
     __syncthreads();
 #pragma unroll
     for (int xx = 0; xx < RK; ++xx)
 #pragma unroll
       for (int y = 0; y < 2; ++y) s[xx][y] *= gam;
-    product<RK, 2>(C, Xs, 1, KP, Zs, VP, 1, s);
+    product<RK, 2>(C, Ks, 1, KP, Vs, VP, 1, s);
   }
-  if (S_end) {
+  if (!PAR && p.S_out) {
 #pragma unroll
     for (int xx = 0; xx < RK; ++xx)
 #pragma unroll
-      for (int y = 0; y < 2; ++y) S_end[bh * sblk + (size_t)(r0 + 16 * xx) * Dv + j0 + c0 + 16 * y] = s[xx][y];
+      for (int y = 0; y < 2; ++y)
+        p.S_out[bh * sblk + (size_t)(r0 + 16 * xx) * Dv + j0 + c0 + 16 * y] = s[xx][y];
   }
-}
-
-template <int DK, bool OUT>
-constexpr size_t scan_smem() {
-  return sizeof(float) * (C * (DK + 1) + C * (NV + 1) + (OUT ? DK * (NV + 1) + C * (DK + 1) + 2 * C * CP : 0));
 }
 
 // --------------------------------------------------------------- gradient --
@@ -366,39 +428,85 @@ constexpr size_t grad_smem() {
   return sizeof(float) * (2 * C * (DK + 1) + 2 * C * (DV + 1) + 3 * C * CP + DK * (DV + 1));
 }
 
-template <int DK, bool REV, bool OUT>
-cudaError_t scan(const GatedProblem& p, float* states, cudaStream_t stream) {
-  auto kern = gated_simt_scan_kernel<DK, REV, OUT>;
-  constexpr size_t smem = scan_smem<DK, OUT>();
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+int chunks(const GatedProblem& p) { return (p.T + C - 1) / C; }
+
+template <typename K>
+cudaError_t prepare(K kern, size_t smem) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+}
+
+template <int DK, bool PAR>
+cudaError_t outputs(const GatedProblem& p, const float* states, cudaStream_t stream) {
+  auto kern = gated_simt_out_kernel<DK, PAR>;
+  constexpr size_t smem = sizeof(float) * (2 * C * (DK + 1) + (C + DK) * (NV + 1) + 2 * C * CP);
+  cudaError_t e = prepare(kern, smem);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)((size_t)p.B * p.H * (p.Dv / NV)), kThreads, smem, stream>>>(p, states);
+  const size_t grid = (size_t)p.B * p.H * (p.Dv / NV) * (PAR ? chunks(p) : 1);
+  kern<<<(unsigned)grid, kThreads, smem, stream>>>(p, states);
   return cudaGetLastError();
+}
+
+// The state between all chunks: S, and with both directions R.
+template <int DK, int DV>
+cudaError_t states(const GatedProblem& p, float* S, float* R, float* gammas, cudaStream_t stream) {
+  auto kern = gated_simt_local_kernel<DK, DV>;
+  constexpr size_t smem = sizeof(float) * C * (DK + DV + 2);
+  cudaError_t e = prepare(kern, smem);
+  if (e != cudaSuccess) return e;
+  const unsigned dirs = R ? 2 : 1;
+  const size_t BH = (size_t)p.B * p.H;
+  kern<<<dim3((unsigned)(BH * chunks(p)), dirs), kThreads, smem, stream>>>(p, S, R, gammas);
+  gated_simt_between_kernel<<<dim3((unsigned)(BH * (DK * DV / 4 / kThreads)), dirs), kThreads, 0, stream>>>(p, S, R,
+                                                                                                          gammas);
+  return cudaGetLastError();
+}
+
+cudaError_t states_of(const GatedProblem& p, float* S, float* R, float* gammas, cudaStream_t stream) {
+  if (p.Dk == 128) return p.Dv == 128 ? states<128, 128>(p, S, R, gammas, stream) : states<128, 64>(p, S, R, gammas, stream);
+  return p.Dv == 128 ? states<64, 128>(p, S, R, gammas, stream) : states<64, 64>(p, S, R, gammas, stream);
 }
 
 template <int DK, int DV>
 cudaError_t grad(const GatedProblem& p, const float* S, const float* R, cudaStream_t stream) {
   auto kern = gated_simt_grad_kernel<DK, DV>;
   constexpr size_t smem = grad_smem<DK, DV>();
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = prepare(kern, smem);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)((size_t)p.B * p.H * ((p.T + C - 1) / C)), kThreads, smem, stream>>>(p, S, R);
+  kern<<<(unsigned)((size_t)p.B * p.H * chunks(p)), kThreads, smem, stream>>>(p, S, R);
   return cudaGetLastError();
 }
 
+size_t gamma_floats(size_t BH, int T) { return (BH * ((T + C - 1) / C) + 63) / 64 * 64; }
+
 }  // namespace
 
+bool gated_simt_walks(int BH, int T, int Dv, int sms) {
+  return T <= C || (long long)BH * (Dv / NV) >= 2LL * sms;
+}
+
+size_t gated_simt_bytes(int BH, int T, int Dk, int Dv, int directions) {
+  const size_t nch = ((size_t)T + C - 1) / C;
+  return sizeof(float) * (gamma_floats(BH, T) + directions * BH * nch * Dk * Dv);
+}
+
 cudaError_t launch_gated_simt_fwd(const GatedProblem& p, cudaStream_t stream) {
-  return p.Dk == 128 ? scan<128, false, true>(p, nullptr, stream) : scan<64, false, true>(p, nullptr, stream);
+  if (!p.scratch)
+    return p.Dk == 128 ? outputs<128, false>(p, nullptr, stream) : outputs<64, false>(p, nullptr, stream);
+  float* gammas = static_cast<float*>(p.scratch);
+  float* S = gammas + gamma_floats((size_t)p.B * p.H, p.T);
+  const cudaError_t e = states_of(p, S, nullptr, gammas, stream);
+  if (e != cudaSuccess) return e;
+  return p.Dk == 128 ? outputs<128, true>(p, S, stream) : outputs<64, true>(p, S, stream);
 }
 
 cudaError_t launch_gated_simt_bwd(const GatedProblem& p, cudaStream_t stream) {
-  const size_t n = (size_t)p.B * p.H * ((p.T + C - 1) / C) * p.Dk * p.Dv;
-  float* S = static_cast<float*>(p.scratch);
-  float* R = S + n;
-  cudaError_t e = p.Dk == 128 ? scan<128, false, false>(p, S, stream) : scan<64, false, false>(p, S, stream);
-  if (e == cudaSuccess)
-    e = p.Dk == 128 ? scan<128, true, false>(p, R, stream) : scan<64, true, false>(p, R, stream);
+  const size_t BH = (size_t)p.B * p.H;
+  float* gammas = static_cast<float*>(p.scratch);
+  float* S = gammas + gamma_floats(BH, p.T);
+  float* R = S + BH * chunks(p) * p.Dk * p.Dv;
+  GatedProblem b = p;
+  b.S_out = nullptr;
+  const cudaError_t e = states_of(b, S, R, gammas, stream);
   if (e != cudaSuccess) return e;
   if (p.Dk == 128) return p.Dv == 128 ? grad<128, 128>(p, S, R, stream) : grad<128, 64>(p, S, R, stream);
   return p.Dv == 128 ? grad<64, 128>(p, S, R, stream) : grad<64, 64>(p, S, R, stream);
