@@ -847,15 +847,16 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 // r and e hold to float32, the outputs themselves to one rounding of A or B.
 //
 // One CTA per (b, h, chunk), everything in shared memory at once except the
-// states, which pass through one tile (R hi, S hi) and through A's (R lo, S
-// lo, once dV has been staged there and stored).  Every barrier is used once.
+// states: R hi and S hi follow one another in a tile of their own, R lo comes to
+// A's place before A is made, S lo to V's when V has been read; so every load
+// but the first is under way while the epilogue makes A and B.  dV and dK are
+// staged over A, dQ over Q.  Every barrier is used once.
 //   warp 0 TMA, warp 1 MMA, warps 4-11 epilogues (two warps to 32 rows, each
 //   half of the columns), warps 12-19 <S, R> (R in registers) and the sums
 constexpr int kGradThreads = 20 * 32, kGradPlain = 12 * 32, kBarE = 1, kBarT = 2;
 enum : uint32_t {  // single-use mbarriers
   G_QK = 0, G_VO = 8, G_RH = 16, G_RL = 24, G_SH = 32, G_SL = 40, G_SC = 48, G_P = 56, G_DV = 64, G_XR = 72,
-  G_DK = 80, G_DQ = 88, G_ACCFREE = 96, G_PAFREE = 104, G_RHREAD = 112, G_RLREAD = 120, G_DOTS = 128, G_FIN = 136,
-  G_TMEM = 144
+  G_DK = 80, G_DQ = 88, G_ACCFREE = 96, G_RHREAD = 104, G_RLREAD = 112, G_DOTS = 120, G_FIN = 128, G_TMEM = 136
 };
 template <int DK, int DV>
 struct GradLayout {
@@ -864,8 +865,7 @@ struct GradLayout {
   static constexpr uint32_t Q_OFF = 0, K_OFF = Q_OFF + KB * kBlk, V_OFF = K_OFF + KB * kBlk, O_OFF = V_OFF + VB * kBlk;
   static constexpr uint32_t PA_OFF = O_OFF + VB * kBlk, PB_OFF = PA_OFF + 2 * kBlk, X_OFF = PB_OFF + 2 * kBlk;
   static constexpr uint32_t END = X_OFF + STATE;
-  static constexpr uint32_t DK_OFF = KB <= VB ? V_OFF : END;  // dK is staged over V where it fits
-  static constexpr uint32_t SUF_OFF = END + (KB <= VB ? 0 : KB * kBlk);  // suf[128], block products [4]
+  static constexpr uint32_t SUF_OFF = END;  // suf[128], block products [4]
   static constexpr uint32_t THR_OFF = SUF_OFF + 132 * 4;                 // <S, R> of 8 warps, gamma
   static constexpr uint32_t BAR_OFF = (THR_OFF + 9 * 4 + 7) / 8 * 8;
   static constexpr uint32_t BYTES = BAR_OFF + 152;
@@ -873,9 +873,10 @@ struct GradLayout {
   // the rows' sums at the end, over dO: F[2][128], e[2][128], column sums [4][128]
   static constexpr uint32_t FSUM = O_OFF, ESUM = FSUM + 1024, CSUM = ESUM + 1024;
   static_assert(ALLOC <= 232448, "shared memory budget");
+  static_assert(STATE <= VB * kBlk && STATE <= 2 * kBlk, "the states' places");
   static_assert(END % 1024 == 0, "128-byte swizzle atoms stay aligned");
 };
-// TMEM: scores and dO V^T, then dK's two parts | dV's, then dQ's
+// TMEM: scores, then A^T dO, then B K | dO V^T, then B^T Q | V R^T | K R, then dO S^T
 constexpr uint32_t TG_A = 0, TG_B = 128, TG_C = 256, TG_D = 384;
 
 // Sums of 16 columns over the warp's rows: lane l < 16 ends with the sum of
@@ -951,7 +952,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   const float* alpha = GATED ? alpha_all + (size_t)bh * T : nullptr;
 
   if (tid == 0) {
-    for (uint32_t b : {G_QK, G_VO, G_RH, G_RL, G_SH, G_SL, G_SC, G_DV, G_XR, G_DK, G_DQ, G_PAFREE, G_FIN})
+    for (uint32_t b : {G_QK, G_VO, G_RH, G_RL, G_SH, G_SL, G_SC, G_DV, G_XR, G_DK, G_DQ, G_FIN})
       mbar_init(bar + b, 1);
     for (uint32_t b : {G_P, G_ACCFREE, G_RHREAD, G_RLREAD, G_DOTS}) mbar_init(bar + b, 8);  // one arrival per warp
     fence_mbar_init();
@@ -999,15 +1000,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         tma_load_3d(sb + L::V_OFF + i * kBlk, &tmV, bar + G_VO, 64 * i, t0, bh);
       }
       state(G_RH, &tmR, L::X_OFF, at);
-      if (GATED) {
-        bool ok = wait(G_PAFREE);
-        if (ok) state(G_RL, &tmR, L::PA_OFF, at + 1);
-        ok = ok && wait(G_XR) && wait(G_RHREAD);
-        if (ok) state(G_SH, &tmS, L::X_OFF, at);
-        ok = ok && wait(G_DK) && wait(G_RLREAD);
-        if (ok) state(G_SL, &tmS, L::PA_OFF, at + 1);
-      } else {
-        if (wait(G_XR)) state(G_SH, &tmS, L::X_OFF, at);
+      if (GATED) state(G_RL, &tmR, L::PA_OFF, at + 1);
+      if (wait(G_XR)) {  // the products with R (and V) have run
+        if (GATED) state(G_SL, &tmS, L::V_OFF, at + 1);
+        if (!GATED || wait(G_RHREAD)) state(G_SH, &tmS, L::X_OFF, at);
       }
       // never leave with copies in flight
       for (int i = 0; i < n; ++i) (void)wait_bar(bar + got[i], 0, wc);
@@ -1053,38 +1049,37 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     if (ok) {
       tc_fence_after();
-      kn(TG_C, L::K_OFF, L::X_OFF, L::SBLK, DK, DV);  // K R
-      ok = wait_all(G_P);
-    }
-    if (ok) {
-      tc_fence_after();
-      nn(TG_D, L::PA_OFF, L::O_OFF, DV);  // A^T dO
-      mma_commit_elect(bar + G_DV);
-      // dK's parts take the scores' place, which the epilogue has read
-      kk(TG_A, L::V_OFF, kBlk, L::X_OFF, L::SBLK, DV, DK, 0);  // V R^T, hi
-      mma_commit_elect(bar + G_XR);
-      nn(TG_B, L::PB_OFF, L::Q_OFF, DK);  // B^T Q
+      kn(TG_D, L::K_OFF, L::X_OFF, L::SBLK, DK, DV);           // K R
+      kk(TG_C, L::V_OFF, kBlk, L::X_OFF, L::SBLK, DV, DK, 0);  // V R^T, hi
       if (GATED) {
         ok = wait_all(G_RL);
         if (ok) {
           tc_fence_after();
-          kk(TG_A, L::V_OFF, kBlk, L::PA_OFF, L::SBLK, DV, DK, 1);  // V R^T, lo
+          kk(TG_C, L::V_OFF, kBlk, L::PA_OFF, L::SBLK, DV, DK, 1);  // V R^T, lo
         }
       }
     }
     if (ok) {
+      mma_commit_elect(bar + G_XR);
+      ok = wait_all(G_P);
+    }
+    if (ok) {
+      tc_fence_after();
+      nn(TG_A, L::PA_OFF, L::O_OFF, DV);  // A^T dO
+      mma_commit_elect(bar + G_DV);
+      nn(TG_B, L::PB_OFF, L::Q_OFF, DK);  // B^T Q
       mma_commit_elect(bar + G_DK);
       ok = wait_all(G_ACCFREE) && wait_all(G_SH);  // dV's parts have been read
     }
     if (ok) {
       tc_fence_after();
-      kn(TG_D, L::PB_OFF, L::K_OFF, kBlk, C, DK);              // B K
-      kk(TG_C, L::O_OFF, kBlk, L::X_OFF, L::SBLK, DV, DK, 0);  // dO S^T, hi
+      kn(TG_A, L::PB_OFF, L::K_OFF, kBlk, C, DK);              // B K
+      kk(TG_D, L::O_OFF, kBlk, L::X_OFF, L::SBLK, DV, DK, 0);  // dO S^T, hi
       if (GATED) {
         ok = wait_all(G_SL);
         if (ok) {
           tc_fence_after();
-          kk(TG_C, L::O_OFF, kBlk, L::PA_OFF, L::SBLK, DV, DK, 1);  // dO S^T, lo
+          kk(TG_D, L::O_OFF, kBlk, L::V_OFF, L::SBLK, DV, DK, 1);  // dO S^T, lo
         }
       }
     }
@@ -1117,60 +1112,65 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     bool ok = named_bar_and(kBarE, 256, wait(G_SC));
     if (ok) {
       tc_fence_after();
+      float run = 0.f;
+      bool room = false;  // A's place is free of R lo
+#pragma unroll 1
+      for (int pc = 3; pc >= 0; --pc) {  // 16 columns at a time, the right ones first
+        const int c0 = 64 * half + 16 * pc, cb = c0 >> 5;
+        uint32_t pa[8], pb[8];
+        if (cb <= w) {
+          uint32_t x[16], y[16];
+          float m[16];
+          tmem_ld16(lanes + TG_A + c0, x);
+          tmem_ld16(lanes + TG_B + c0, y);
+          if (GATED && cb < w) {
+            float mid = pre;
+            if (cb + 1 < w) mid *= blk[w - 1];
+            if (cb + 2 < w) mid *= blk[w - 2];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int cb = 2 * half + b;
-        float mid = pre, run = 1.f;
-        if (GATED)
-          for (int u = cb + 1; u < w; ++u) mid *= blk[u];
+            for (int j = 0; j < 16; ++j) m[j] = mid * suf[c0 + j];
+          } else {  // the product of alpha over (column, row], zero right of the diagonal
+            const int b0 = c0 & 31;
 #pragma unroll
-        for (int pc = 1; pc >= 0; --pc) {  // 16 columns at a time, the right ones first
-          const int c0 = 32 * cb + 16 * pc;
-          uint32_t pa[8], pb[8];
-          if (cb <= w) {
-            uint32_t x[16], y[16];
-            float m[16];
-            tmem_ld16(lanes + TG_A + c0, x);
-            tmem_ld16(lanes + TG_B + c0, y);
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 14; j >= 0; j -= 2) {
-              float va[2], vb[2];
-#pragma unroll
-              for (int h = 1; h >= 0; --h) {
-                const int jj = 16 * pc + j + h;  // column in the block
-                float f = 1.f;
-                if (cb < w) {
-                  if (GATED) f = mid * suf[c0 + j + h];
-                } else {
-                  if (GATED && jj < 31) {
-                    const float t = __shfl_sync(0xffffffffu, a, jj < 31 ? jj + 1 : 31);
-                    run = jj < lane ? run * t : 1.f;
-                  }
-                  f = run;
-                }
-                const bool in = cb < w || jj <= lane;
-                const float s = __uint_as_float(x[j + h]), o = __uint_as_float(y[j + h]);
-                va[h] = in ? s * f : 0.f;
-                vb[h] = in ? o * f : 0.f;
-                m[j + h] = cb < w || jj < lane ? s * vb[h] : 0.f;
-                if (GATED) fsum += m[j + h];
+            for (int j = 15; j >= 0; --j) {
+              if (GATED) {
+                const float t = __shfl_sync(0xffffffffu, a, b0 + j + 1);
+                run = b0 + j == lane ? 1.f : run * t;
+                m[j] = run;
+              } else {
+                m[j] = cb < w || b0 + j <= lane ? 1.f : 0.f;
               }
-              pa[j / 2] = pack2_bf16(va[0], va[1]);
-              pb[j / 2] = pack2_bf16(vb[0], vb[1]);
             }
-            if (GATED) csum[2 * b + pc] = fold16(m);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) pa[i] = pb[i] = 0;
           }
+          tmem_wait_ld();
+          const int diag = cb == w ? lane - (c0 & 31) : -1;  // the diagonal's column of the piece
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int col = c0 + 8 * h;
-            const uint32_t at = (uint32_t)(col >> 6) * kBlk + sw128_off(row, (col >> 3) & 7);
-            *reinterpret_cast<uint4*>(sm + L::PA_OFF + at) = make_uint4(pa[4 * h], pa[4 * h + 1], pa[4 * h + 2], pa[4 * h + 3]);
-            *reinterpret_cast<uint4*>(sm + L::PB_OFF + at) = make_uint4(pb[4 * h], pb[4 * h + 1], pb[4 * h + 2], pb[4 * h + 3]);
+          for (int j = 0; j < 16; j += 2) {
+            const float s0 = __uint_as_float(x[j]), s1 = __uint_as_float(x[j + 1]);
+            const float b0 = __uint_as_float(y[j]) * m[j], b1 = __uint_as_float(y[j + 1]) * m[j + 1];
+            pa[j / 2] = pack2_bf16(s0 * m[j], s1 * m[j + 1]);
+            pb[j / 2] = pack2_bf16(b0, b1);
+            m[j] = j == diag ? 0.f : s0 * b0;
+            m[j + 1] = j + 1 == diag ? 0.f : s1 * b1;
+            if (GATED) fsum += m[j] + m[j + 1];
           }
+          if (GATED) {
+            const float v = fold16(m);
+            csum[0] = pc == 0 ? v : csum[0];
+            csum[1] = pc == 1 ? v : csum[1];
+            csum[2] = pc == 2 ? v : csum[2];
+            csum[3] = pc == 3 ? v : csum[3];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) pa[i] = pb[i] = 0;
+        }
+        if (GATED && !room) room = wait(G_XR) && wait(G_RLREAD);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t at = (uint32_t)half * kBlk + sw128_off(row, 2 * pc + h);
+          *reinterpret_cast<uint4*>(sm + L::PA_OFF + at) = make_uint4(pa[4 * h], pa[4 * h + 1], pa[4 * h + 2], pa[4 * h + 3]);
+          *reinterpret_cast<uint4*>(sm + L::PB_OFF + at) = make_uint4(pb[4 * h], pb[4 * h + 1], pb[4 * h + 2], pb[4 * h + 3]);
         }
       }
       tc_fence_before();
@@ -1181,7 +1181,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     if (ok) {
       tc_fence_after();
-      grad_row<DV / 2, false>(lanes + TG_C, lanes + TG_D, out, nullptr, sm + L::PA_OFF, row, half * (DV / 2));
+      grad_row<DV / 2, false>(lanes + TG_D, lanes + TG_A, out, nullptr, sm + L::PA_OFF, row, half * (DV / 2));
       tc_fence_before();
       arrive(G_ACCFREE);
       fence_proxy_async_smem();
@@ -1191,20 +1191,19 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         for (int i = 0; i < VB; ++i) tma_store_3d(&tmDV, sb + L::PA_OFF + i * kBlk, 64 * i, t0, bh);
         bulk_commit_group();
         bulk_wait_group_read<0>();
-        mbar_arrive(bar + G_PAFREE);
       }
       __syncwarp();
       ok = named_bar_and(kBarE, 256, wait(G_DK));
     }
     if (ok) {
-      // ---- dK ----
+      // ---- dK, staged there too ----
       tc_fence_after();
-      esum = grad_row<DK / 2, GATED>(lanes + TG_A, lanes + TG_B, out, sm + L::K_OFF, sm + L::DK_OFF, row, half * (DK / 2));
+      esum = grad_row<DK / 2, GATED>(lanes + TG_C, lanes + TG_B, out, sm + L::K_OFF, sm + L::PA_OFF, row, half * (DK / 2));
       fence_proxy_async_smem();
       named_bar_sync(kBarE, 256);
       if (leader) {
 #pragma unroll
-        for (int i = 0; i < KB; ++i) tma_store_3d(&tmDK, sb + L::DK_OFF + i * kBlk, 64 * i, t0, bh);
+        for (int i = 0; i < KB; ++i) tma_store_3d(&tmDK, sb + L::PA_OFF + i * kBlk, 64 * i, t0, bh);
         bulk_commit_group();
       }
       __syncwarp();
@@ -1213,7 +1212,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     if (ok) {
       // ---- dQ, staged over Q (each thread over what it has read) ----
       tc_fence_after();
-      fsum += grad_row<DK / 2, GATED>(lanes + TG_C, lanes + TG_D, into, sm + L::Q_OFF, sm + L::Q_OFF, row, half * (DK / 2));
+      fsum += grad_row<DK / 2, GATED>(lanes + TG_D, lanes + TG_A, into, sm + L::Q_OFF, sm + L::Q_OFF, row, half * (DK / 2));
       if (GATED) {  // dO has been read
         reinterpret_cast<float*>(sm + L::FSUM)[half * C + row] = fsum;
         reinterpret_cast<float*>(sm + L::ESUM)[half * C + row] = esum;
@@ -1265,7 +1264,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           float x[8];
-          piece(part ? L::PA_OFF : L::X_OFF, i, x);
+          piece(part ? L::V_OFF : L::X_OFF, i, x);
 #pragma unroll
           for (int e = 0; e < 8; ++e) dot = fmaf(x[e], r[i][e], dot);
         }
