@@ -417,6 +417,28 @@ def test_same_bits_twice_and_nothing_outside(dn, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("T", [5, 300])
+def test_sixteen_byte_alignment(dn, T):
+    """Every buffer at an odd multiple of 16 bytes."""
+    x = case(2, 2, T, 64, 128, torch.bfloat16, "mixed", True, T)
+
+    def shifted(t):
+        n = 16 // t.element_size()
+        buf = torch.empty(t.numel() + n, dtype=t.dtype, device="cuda")
+        buf[n:].copy_(t.reshape(-1))
+        assert buf[n:].data_ptr() % 32 == 16
+        return buf[n:].view(t.shape)
+
+    want = dn.gated_linear_attn_fwd(*pick(x, FWD)), dn.gated_linear_attn_bwd(*pick(x, BWD))
+    y = {n: shifted(t) for n, t in x.items()}
+    o, S = shifted(x["v"]), shifted(x["S0"])
+    dn.gated_linear_attn_fwd(*pick(y, FWD), o=o, S_out=S)
+    assert torch.equal(o, want[0][0]) and torch.equal(S, want[0][1])
+    got = dn.gated_linear_attn_bwd(*pick(y, BWD))
+    assert all(torch.equal(got[n], want[1][n]) for n in got)
+
+
+@gpu
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_nan_stays_in_its_head_and_behind_its_chunk(dn, dtype):
     x = case(1, 3, 400, 64, 64, dtype, "mixed", False, 14)
