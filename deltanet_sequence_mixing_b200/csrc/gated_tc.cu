@@ -77,17 +77,17 @@ struct OutLayout {
   static constexpr uint32_t ALLOC = BYTES + 1024;
   static_assert(ALLOC <= 232448, "shared memory budget");
 };
-// Of the state kernel: NST stages of X and Z, the scaled copy, the stored state.
-constexpr int NST = 3;
+// Of the state kernel: two stages of X and Z, the scaled copy of Z twice, the
+// stored state.
 template <int DK>
 struct StateLayout {
   static constexpr int KB = DK / 64;
-  static constexpr uint32_t X_OFF = 0;  // [NST][KB] blocks
-  static constexpr uint32_t Z_OFF = X_OFF + NST * KB * kBlk;
-  static constexpr uint32_t VT_OFF = Z_OFF + NST * kBlk;
-  static constexpr uint32_t ST_OFF = VT_OFF + 2 * kBlk;  // hi, lo: DK rows x 128 bytes each
+  static constexpr uint32_t X_OFF = 0;  // [2][KB] blocks
+  static constexpr uint32_t Z_OFF = X_OFF + 2 * KB * kBlk;
+  static constexpr uint32_t VT_OFF = Z_OFF + 2 * kBlk;   // [2]: hi, lo
+  static constexpr uint32_t ST_OFF = VT_OFF + 4 * kBlk;  // hi, lo: DK rows x 128 bytes each
   static constexpr uint32_t BAR_OFF = ST_OFF + 2 * DK * 128;
-  static constexpr uint32_t BYTES = BAR_OFF + 256;
+  static constexpr uint32_t BYTES = BAR_OFF + 128;
   static constexpr uint32_t ALLOC = BYTES + 1024;
   static_assert(ALLOC <= 232448, "shared memory budget");
 };
@@ -99,10 +99,8 @@ enum : uint32_t {
   B_FULLK = 0, B_FULLQ = 16, B_FULLV = 32, B_SC = 56, B_P = 72, B_VT = 88, B_DS = 104, B_DSFREE = 120, B_S = 136,
   B_QS = 152, B_PV = 168, B_OFREE = 184, B_VFREE = 200, B_DECAY = 224, B_FIN = 248, B_TMEM = 264
 };
-// of the state kernel: C_FULL and C_FREE one per stage
-enum : uint32_t {
-  C_FULL = 0, C_FREE = 24, C_VT = 48, C_DS = 64, C_DSFREE = 80, C_FIN = 96, C_TMEM = 104
-};
+// of the state kernel, two per name (chunk parity)
+enum : uint32_t { C_FULL = 0, C_FREE = 16, C_VT = 32, C_DS = 48, C_DSFREE = 64, C_FIN = 80, C_TMEM = 88 };
 
 // mbar_wait made short, its limit in polls instead of nanoseconds.  The roles of
 // a kernel run different code at the same time and wait at some thirty places;
@@ -259,24 +257,25 @@ __device__ __forceinline__ void scale_row(const uint8_t* tile, uint8_t* hi, uint
   }
 }
 
-// The 64 columns of this thread's state row, entering segment g: the caller's
+// NC columns of this thread's state row, entering segment g: the caller's
 // state and the segments passed before it in the scan's direction.
-template <int DK, bool REV>
-__device__ __forceinline__ void enter_state(const GatedScan& p, size_t bh, int g, int j0, int row, float (&s)[NV]) {
+template <int DK, int NC>
+__device__ __forceinline__ void enter_state(const GatedScan& p, bool rev, size_t bh, int g, int j0, int row,
+                                            float (&s)[NC]) {
   const size_t sblk = (size_t)DK * p.Dv, at = (size_t)row * p.Dv + j0;
   const float* src = p.S_in ? p.S_in + bh * p.S_in_stride + at : nullptr;
 #pragma unroll
-  for (int j = 0; j < NV; j += 4) {
+  for (int j = 0; j < NC; j += 4) {
     const float4 v = src ? *reinterpret_cast<const float4*>(src + j) : make_float4(0.f, 0.f, 0.f, 0.f);
     s[j] = v.x; s[j + 1] = v.y; s[j + 2] = v.z; s[j + 3] = v.w;
   }
-  const int n = REV ? p.G - 1 - g : g;
+  const int n = rev ? p.G - 1 - g : g;
   for (int i = 0; i < n; ++i) {
-    const size_t u = bh * p.G + (REV ? p.G - 1 - i : i);
+    const size_t u = bh * p.G + (rev ? p.G - 1 - i : i);
     const float gam = p.seg_decay[u];
     const float4* e = reinterpret_cast<const float4*>(p.seg_end + u * sblk + at);
 #pragma unroll
-    for (int j = 0; j < NV; j += 4) {
+    for (int j = 0; j < NC; j += 4) {
       const float4 v = __ldg(e + j / 4);
       s[j] = fmaf(gam, s[j], v.x);
       s[j + 1] = fmaf(gam, s[j + 1], v.y);
@@ -285,17 +284,18 @@ __device__ __forceinline__ void enter_state(const GatedScan& p, size_t bh, int g
     }
   }
 }
-__device__ __forceinline__ void leave_state(float* dst, const float (&s)[NV]) {
+template <int NC>
+__device__ __forceinline__ void leave_state(float* dst, const float (&s)[NC]) {
 #pragma unroll
-  for (int j = 0; j < NV; j += 4)
+  for (int j = 0; j < NC; j += 4)
     *reinterpret_cast<float4*>(dst + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
 }
 
 // s <- gamma s + this lane's increment (its hi and lo halves at taddr, + 64)
-template <bool GATED>
-__device__ __forceinline__ void add_increment(float (&s)[NV], float gamma, uint32_t taddr) {
+template <bool GATED, int NC>
+__device__ __forceinline__ void add_increment(float (&s)[NC], float gamma, uint32_t taddr) {
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
+  for (int h = 0; h < NC / 16; ++h) {
     uint32_t x[16], y[16];
     tmem_ld16(taddr + 16 * h, x);
     if (GATED) tmem_ld16(taddr + 64 + 16 * h, y);
@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float s[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) s[j] = 0.f;
-    if (live) enter_state<DK, false>(p, bh, g, j0, row, s);
+    if (live) enter_state<DK>(p, false, bh, g, j0, row, s);
     auto put = [&]() {
       if (live) {
 #pragma unroll
@@ -661,40 +661,43 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------ state kernel --
-// x = k, z = v (forward) or x = q, z = dO from the end (REV); the segments'
-// end states from zero (STORE = false), or every chunk's entry state in the
-// scan's direction as bf16 hi and lo, from the segment's true entry (STORE).
-constexpr int kStateThreads = 12 * 32;  // TMA 0, MMA 1, state 4-7, scaling 8-11
-template <int DK, bool GATED, bool REV, bool STORE>
+// Forward (blockIdx.y = 0: x = k, z = v) and from the end (1: x = q, z = dO):
+// the segments' end states from zero (STORE = false), or every chunk's entry
+// state in the scan's direction as bf16 hi and lo, from the segment's true entry
+// (STORE).  With the scaled Z twice, scaling a chunk runs beside the products of
+// the one before; what is left is bound by what a chunk moves through shared
+// memory (copies in and out, the scaled Z, the operands).
+constexpr int kStateThreads = 20 * 32;  // TMA 0, MMA 1, state 4-11, scaling 12-19
+template <int DK, bool GATED, bool STORE>
 __global__ void __launch_bounds__(kStateThreads, 1)
-    gated_state_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmZ,
-                       const __grid_constant__ CUtensorMap tmS, const GatedScan p) {
+    gated_state_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmQ,
+                       const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmR,
+                       const __grid_constant__ GatedScan fwd, const __grid_constant__ GatedScan rvs) {
   using L = StateLayout<DK>;
   constexpr int KB = L::KB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = warp_uniform(smem_u32(sm));
   const int tid = threadIdx.x, lane = tid & 31, warp = (int)warp_uniform((uint32_t)tid >> 5), w = warp & 3;
+  const bool rev = blockIdx.y;
+  const GatedScan& p = rev ? rvs : fwd;
   const int nsl = p.Dv / NV, T = p.T, segs = STORE ? p.G : p.G - 1;
   const int slice = blockIdx.x % nsl, bh = blockIdx.x / nsl / segs;
   // without STORE the scan's last segment is not needed
-  const int g = (int)(blockIdx.x / nsl) % segs + (!STORE && REV ? 1 : 0);
+  const int g = (int)(blockIdx.x / nsl) % segs + (!STORE && rev ? 1 : 0);
   const int j0 = slice * NV, nch = (T + C - 1) / C;
   const int first = g * p.seg_chunks, n = min(p.seg_chunks, nch - first);
-  auto chunk = [&](int i) { return REV ? first + n - 1 - i : first + i; };
+  auto chunk = [&](int i) { return rev ? first + n - 1 - i : first + i; };
   const uint32_t bar = sb + L::BAR_OFF;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::BAR_OFF + C_TMEM);
   const float* alpha = GATED ? p.alpha + (size_t)bh * T : nullptr;
 
   if (tid == 0) {
-    for (uint32_t i = 0; i < (uint32_t)NST; ++i) {
-      mbar_init(bar + C_FULL + 8 * i, 1);
-      mbar_init(bar + C_FREE + 8 * i, 1);
-    }
     for (uint32_t i = 0; i < 2; ++i) {
-      mbar_init(bar + C_VT + 8 * i, 4);
-      mbar_init(bar + C_DS + 8 * i, 1);
-      mbar_init(bar + C_DSFREE + 8 * i, 4);
+      for (uint32_t b : {C_FULL, C_FREE, C_DS}) mbar_init(bar + b + 8 * i, 1);
+      mbar_init(bar + C_VT + 8 * i, 8);
+      mbar_init(bar + C_DSFREE + 8 * i, 8);
     }
     mbar_init(bar + C_FIN, 1);
     fence_mbar_init();
@@ -707,67 +710,65 @@ __global__ void __launch_bounds__(kStateThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = warp_uniform(*tmem_slot);
-  unsigned int* const wc = p.status;
-  auto wait2 = [&](uint32_t b, int i) {  // a barrier pair by parity
-    return __all_sync(0xffffffffu, wait_bar(bar + b + 8 * (i & 1), (i >> 1) & 1, wc)) != 0;
-  };
-  auto wait_stage = [&](uint32_t b, int i) { return wait_bar(bar + b + 8 * (i % NST), (i / NST) & 1, wc); };
+  auto done = [&](uint32_t b, int i) { return wait_bar(bar + b + 8 * (i & 1), (i >> 1) & 1, p.status); };
+  auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
 
   if (warp == kWarpTma) {
     if (lane == 0) {
-      prefetch_tmap(&tmX);
-      prefetch_tmap(&tmZ);
+      const CUtensorMap* mx = rev ? &tmQ : &tmK;
+      const CUtensorMap* mz = rev ? &tmO : &tmV;
+      prefetch_tmap(mx);
+      prefetch_tmap(mz);
       int issued = 0;
       for (int i = 0; i < n; ++i) {
-        const int s = i % NST, row = chunk(i) * C;
-        if (i >= NST && !wait_stage(C_FREE, i - NST)) break;
+        const int s = i & 1, row = chunk(i) * C;
+        if (i >= 2 && !done(C_FREE, i - 2)) break;
         const uint32_t f = bar + C_FULL + 8 * s;
         mbar_expect_tx(f, (KB + 1) * kBlk);
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) tma_load_3d(sb + L::X_OFF + (s * KB + kb) * kBlk, &tmX, f, kb * 64, row, bh);
-        tma_load_3d(sb + L::Z_OFF + s * kBlk, &tmZ, f, j0, row, bh);
+        for (int kb = 0; kb < KB; ++kb)
+          tma_load_3d(sb + L::X_OFF + (s * KB + kb) * kBlk, mx, f, kb * 64, row, bh);
+        tma_load_3d(sb + L::Z_OFF + s * kBlk, mz, f, j0, row, bh);
         issued = i + 1;
       }
       // never leave with copies in flight
-      for (int i = issued > NST ? issued - NST : 0; i < issued; ++i)
-        (void)wait_bar(bar + C_FULL + 8 * (i % NST), (i / NST) & 1, wc);
+      for (int i = issued > 2 ? issued - 2 : 0; i < issued; ++i) (void)done(C_FULL, i);
     }
   } else if (warp == kWarpMma) {
     bool ok = true;
     for (int i = 0; i < n && ok; ++i) {
-      const int s = i % NST, b = i & 1;
-      ok = (GATED ? wait2(C_VT, i) : __all_sync(0xffffffffu, wait_stage(C_FULL, i)) != 0) &&
-           (i < 2 || wait2(C_DSFREE, i - 2));
+      const int s = i & 1;
+      ok = all(done(GATED ? C_VT : C_FULL, i) && (i < 2 || done(C_DSFREE, i - 2)));
       if (!ok) break;
       tc_fence_after();
       constexpr uint32_t id = idesc_bf16(128, GATED ? 128 : 64, true, true);
       const uint64_t da = desc_mn(sb + L::X_OFF + s * KB * kBlk, kBlk);
-      const uint64_t db = desc_mn(sb + (GATED ? L::VT_OFF : L::Z_OFF + s * kBlk), kBlk);
+      const uint64_t db = desc_mn(sb + (GATED ? L::VT_OFF + s * 2 * kBlk : L::Z_OFF + s * kBlk), kBlk);
 #pragma unroll
       for (int ks = 0; ks < C / 16; ++ks)
-        mma_bf16_ss_elect(tmem + 128 * b, desc_step(da, ks * 2048), desc_step(db, ks * 2048), id, ks > 0);
-      mma_commit_elect(bar + C_DS + 8 * b);
+        mma_bf16_ss_elect(tmem + 128 * s, desc_step(da, ks * 2048), desc_step(db, ks * 2048), id, ks > 0);
       mma_commit_elect(bar + C_FREE + 8 * s);
+      mma_commit_elect(bar + C_DS + 8 * s);
     }
     tc_fence_after();  // no MMA may outlive TMEM
     mma_commit_elect(bar + C_FIN);
-    (void)wait_bar(bar + C_FIN, 0, wc);
-  } else if (warp >= 4 && warp < 8) {
-    const int row = 32 * w + lane;
+    (void)wait_bar(bar + C_FIN, 0, p.status);
+  } else if (warp >= 4 && warp < 12) {
+    const int row = 32 * w + lane, half = (warp - 4) >> 2, jc = j0 + 32 * half;
     const bool live = row < DK, leader = warp == 4 && lane == 0;
-    const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
-    float s[NV], total = 1.f;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16) + 32 * half;
+    const size_t at = (size_t)row * p.Dv + jc, sblk = (size_t)DK * p.Dv;
+    float s[NV / 2], total = 1.f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) s[j] = 0.f;
-    if (STORE && live) enter_state<DK, REV>(p, bh, g, j0, row, s);
+    for (int j = 0; j < NV / 2; ++j) s[j] = 0.f;
+    if (STORE && live) enter_state<DK>(p, rev, bh, g, jc, row, s);
     // The main kernel takes the caller's state from the slot that the last
     // segment leaves unused, so that it may write S_out over S0.
-    if (!STORE && !REV && live && g == 0 && p.S_in) {
-      const size_t at = (size_t)row * p.Dv + j0, sblk = (size_t)DK * p.Dv;
+    if (!STORE && !rev && live && g == 0 && p.S_in) {
       const float4* src = reinterpret_cast<const float4*>(p.S_in + bh * p.S_in_stride + at);
       float4* dst = reinterpret_cast<float4*>(p.seg_end + ((size_t)bh * p.G + p.G - 1) * sblk + at);
 #pragma unroll
-      for (int j = 0; j < NV / 4; ++j) dst[j] = src[j];
+      for (int j = 0; j < NV / 8; ++j) dst[j] = src[j];
     }
     float a[4] = {1.f, 1.f, 1.f, 1.f};
     if (GATED) load_alpha(alpha, T, chunk(0), a);
@@ -778,27 +779,28 @@ __global__ void __launch_bounds__(kStateThreads, 1)
       if (GATED && i + 1 < n) load_alpha(alpha, T, chunk(i + 1), a);
       if (STORE) {
         if (leader) bulk_wait_group_read<0>();  // the staging tiles are free
-        named_bar_sync(kBarS, 128);
+        named_bar_sync(kBarS, 256);
         if (live) {
 #pragma unroll
-          for (int c16 = 0; c16 < 8; ++c16) {
+          for (int c16 = 0; c16 < 4; ++c16) {
             uint4 h, l;
             split8(s + 8 * c16, h, l);
-            *reinterpret_cast<uint4*>(sm + L::ST_OFF + sw128_off(row, c16)) = h;
-            *reinterpret_cast<uint4*>(sm + L::ST_OFF + DK * 128 + sw128_off(row, c16)) = l;
+            *reinterpret_cast<uint4*>(sm + L::ST_OFF + sw128_off(row, 4 * half + c16)) = h;
+            *reinterpret_cast<uint4*>(sm + L::ST_OFF + DK * 128 + sw128_off(row, 4 * half + c16)) = l;
           }
         }
         fence_proxy_async_smem();
-        named_bar_sync(kBarS, 128);
+        named_bar_sync(kBarS, 256);
         if (leader) {
-          const int at = (bh * nch + chunk(i)) * 2;
-          tma_store_3d(&tmS, sb + L::ST_OFF, j0, 0, at);
-          tma_store_3d(&tmS, sb + L::ST_OFF + DK * 128, j0, 0, at + 1);
+          const CUtensorMap* ms = rev ? &tmR : &tmS;
+          const int to = (bh * nch + chunk(i)) * 2;
+          tma_store_3d(ms, sb + L::ST_OFF, j0, 0, to);
+          tma_store_3d(ms, sb + L::ST_OFF + DK * 128, j0, 0, to + 1);
           bulk_commit_group();
         }
       }
-      // with STORE the four warps meet at barriers, so they leave together
-      ok = STORE ? named_bar_and(kBarS, 128, wait_bar(bar + C_DS + 8 * (i & 1), (i >> 1) & 1, wc)) : wait2(C_DS, i);
+      // with STORE the eight warps meet at barriers, so they leave together
+      ok = STORE ? named_bar_and(kBarS, 256, done(C_DS, i)) : all(done(C_DS, i));
       if (!ok) break;
       tc_fence_after();
       add_increment<GATED>(s, gamma, lanes + 128 * (i & 1));
@@ -808,25 +810,25 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     }
     if (leader) bulk_wait_group_all();
     if (ok && live) {
-      const size_t at = (size_t)row * p.Dv + j0, sblk = (size_t)DK * p.Dv;
       if (STORE) {
-        if (p.S_out && g == (REV ? 0 : p.G - 1)) leave_state(p.S_out + (size_t)bh * sblk + at, s);
+        if (p.S_out && g == (rev ? 0 : p.G - 1)) leave_state(p.S_out + (size_t)bh * sblk + at, s);
       } else {
         leave_state(p.seg_end + ((size_t)bh * p.G + g) * sblk + at, s);
         if (leader && slice == 0) p.seg_decay[(size_t)bh * p.G + g] = total;
       }
     }
-  } else if (GATED && warp >= 8) {
-    const int row = 32 * w + lane;
+  } else if (GATED && warp >= 12) {
+    const int row = 32 * w + lane, c16 = 4 * ((warp - 12) >> 2);
     float a[4];
     load_alpha(alpha, T, chunk(0), a);
     bool ok = true;
     for (int i = 0; i < n && ok; ++i) {
-      const float f = REV ? decay_into(a, w) : decay_out(a, w);
+      const float f = rev ? decay_into(a, w) : decay_out(a, w);
       if (i + 1 < n) load_alpha(alpha, T, chunk(i + 1), a);
-      ok = __all_sync(0xffffffffu, wait_stage(C_FULL, i)) && (i < 1 || wait2(C_DS, i - 1));
+      ok = all(done(C_FULL, i) && (i < 2 || done(C_FREE, i - 2)));  // the products have read the copy's place
       if (!ok) break;
-      scale_row(sm + L::Z_OFF + (i % NST) * kBlk, sm + L::VT_OFF, sm + L::VT_OFF + kBlk, row, f, 0, 8);
+      uint8_t* vt = sm + L::VT_OFF + (i & 1) * 2 * kBlk;
+      scale_row(sm + L::Z_OFF + (i & 1) * kBlk, vt, vt + kBlk, row, f, c16, c16 + 4);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar + C_VT + 8 * (i & 1));
@@ -1331,21 +1333,28 @@ cudaError_t launch_out(const GatedProblem& p, const GatedScan& s, cudaStream_t s
   return cudaGetLastError();
 }
 
-// The state kernel over x (BH,T,DK) and z (BH,T,Dv).
-template <int DK, bool GATED, bool REV, bool STORE>
-cudaError_t launch_state(const void* x, const void* z, void* states, int BH, const GatedScan& s, cudaStream_t st) {
-  CUtensorMap mx, mz, ms;
-  const int nch = (s.T + C - 1) / C;
-  if (!make_tmap_3d_bf16(&mx, x, DK, s.T, BH, C) || !make_tmap_3d_bf16(&mz, z, s.Dv, s.T, BH, C))
+// The state kernel: the forward scan, and with `r` the one from the end too.
+template <int DK, bool GATED, bool STORE>
+cudaError_t launch_state(const GatedProblem& p, const GatedScan& f, const GatedScan* r, void* S, void* R,
+                         cudaStream_t st) {
+  CUtensorMap mk, mv, ms, mq, mo, mr;
+  const int BH = p.B * p.H, nch = (p.T + C - 1) / C;
+  if (!make_tmap_3d_bf16(&mk, p.k, DK, p.T, BH, C) || !make_tmap_3d_bf16(&mv, p.v, p.Dv, p.T, BH, C))
     return cudaErrorInvalidValue;
-  ms = mz;
-  if (STORE && !make_tmap_3d_bf16(&ms, states, s.Dv, DK, 2 * BH * nch, DK)) return cudaErrorInvalidValue;
-  auto kern = gated_state_kernel<DK, GATED, REV, STORE>;
+  mq = mk;
+  mo = ms = mr = mv;
+  if (r && (!make_tmap_3d_bf16(&mq, p.q, DK, p.T, BH, C) || !make_tmap_3d_bf16(&mo, p.dO, p.Dv, p.T, BH, C)))
+    return cudaErrorInvalidValue;
+  if (STORE && (!make_tmap_3d_bf16(&ms, S, p.Dv, DK, 2 * BH * nch, DK) ||
+                !make_tmap_3d_bf16(&mr, R, p.Dv, DK, 2 * BH * nch, DK)))
+    return cudaErrorInvalidValue;
+  auto kern = gated_state_kernel<DK, GATED, STORE>;
   constexpr int smem = (int)StateLayout<DK>::ALLOC;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const size_t segs = STORE ? s.G : s.G - 1;
-  kern<<<(unsigned)(BH * segs * (s.Dv / NV)), GATED ? kStateThreads : 256, smem, st>>>(mx, mz, ms, s);
+  const size_t segs = STORE ? f.G : f.G - 1;
+  kern<<<dim3((unsigned)(BH * segs * (p.Dv / NV)), r ? 2 : 1), GATED ? kStateThreads : 12 * 32, smem, st>>>(
+      mk, mv, ms, mq, mo, mr, f, r ? *r : f);
   return cudaGetLastError();
 }
 
@@ -1365,14 +1374,13 @@ GatedScan gated_scan_of(const GatedProblem& p, void* scratch) {
 
 template <int DK, bool GATED>
 cudaError_t fwd(const GatedProblem& p, cudaStream_t st) {
-  const int BH = p.B * p.H;
   GatedScan s = gated_scan_of(p, p.scratch);
   const size_t sblk = (size_t)DK * p.Dv;
   s.S_in = p.S0;
   s.S_in_stride = sblk;
   s.S_out = p.S_out;
   if (s.G > 1) {
-    cudaError_t e = launch_state<DK, GATED, false, false>(p.k, p.v, nullptr, BH, s, st);
+    cudaError_t e = launch_state<DK, GATED, false>(p, s, nullptr, nullptr, nullptr, st);
     if (e != cudaSuccess) return e;
     if (p.S0) {
       s.S_in = s.seg_end + (s.G - 1) * sblk;
@@ -1417,13 +1425,11 @@ cudaError_t bwd(const GatedProblem& p, cudaStream_t st) {
   f.S_in_stride = r.S_in_stride = sblk;
   cudaError_t e = cudaSuccess;
   if (p.G > 1) {
-    GatedScan f0 = f;  // S_out of the scan is the caller's only in the forward
-    f0.S_in = nullptr;
-    e = launch_state<DK, GATED, false, false>(p.k, p.v, nullptr, BH, f0, st);
-    if (e == cudaSuccess) e = launch_state<DK, GATED, true, false>(p.q, p.dO, nullptr, BH, r, st);
+    GatedScan ends = f;  // the caller's state stays where it is: nothing writes over it here
+    ends.S_in = nullptr;
+    e = launch_state<DK, GATED, false>(p, ends, &r, nullptr, nullptr, st);
   }
-  if (e == cudaSuccess) e = launch_state<DK, GATED, false, true>(p.k, p.v, S, BH, f, st);
-  if (e == cudaSuccess) e = launch_state<DK, GATED, true, true>(p.q, p.dO, R, BH, r, st);
+  if (e == cudaSuccess) e = launch_state<DK, GATED, true>(p, f, &r, S, R, st);
   if (e != cudaSuccess) return e;
   return p.Dv == 128 ? launch_grad<DK, 128, GATED>(p, S, R, st) : launch_grad<DK, 64, GATED>(p, S, R, st);
 }
