@@ -539,6 +539,7 @@ int gated_linear_attn_bwd(const void* q, const void* k, const void* v, const flo
   p.scratch = static_cast<uint8_t*>(workspace) + kStatusBytes;
   if (!p.bf16) return map_cuda(dn::launch_gated_simt_bwd(p, st));
   gated_split(B, H, T, Dv, &p.G, &p.seg_chunks);
+  p.sms = sm_count_now();
   return map_cuda(dn::launch_gated_tc_bwd(p, st));
 }
 

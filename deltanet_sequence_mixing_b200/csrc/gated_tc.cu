@@ -855,17 +855,21 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 // chunk, so no error travels along T; dO S^T and V R^T take hi and lo so that
 // r and e hold to float32, the outputs themselves to one rounding of A or B.
 //
-// One CTA per (b, h, chunk), everything in shared memory at once except the
-// states: R hi and S hi follow one another in a tile of their own, R lo comes to
-// A's place before A is made, S lo to V's when V has been read; so every load
-// but the first is under way while the epilogue makes A and B.  dV is staged over A
-// for its TMA store, dK over K, dQ over Q.  Every barrier is used once.
+// One CTA per SM walks over the (b, h, chunk)s.  Everything of a chunk is in
+// shared memory at once except the states: R hi and S hi follow one another in a
+// tile of their own, R lo comes to A's place before A is made, S lo to V's when V
+// has been read.  dV is staged over A for its TMA store, dK over K, dQ over Q.
+// The next chunk's tiles are loaded as their places fall free, while this one's
+// last gradients are made and stored.  Every barrier completes once a chunk.
 //   warp 0 TMA, warp 1 MMA, warps 4-11 epilogues (two warps to 32 rows, each
 //   half of the columns), warps 12-19 <S, R> (R in registers) and the sums
 constexpr int kGradThreads = 20 * 32, kGradPlain = 12 * 32, kBarE = 1, kBarT = 2;
-enum : uint32_t {  // single-use mbarriers
-  G_QK = 0, G_VO = 8, G_RH = 16, G_RL = 24, G_SH = 32, G_SL = 40, G_SC = 48, G_P = 56, G_DV = 64, G_XR = 72,
-  G_DK = 80, G_DQ = 88, G_ACCFREE = 96, G_RHREAD = 104, G_RLREAD = 112, G_DOTS = 120, G_FIN = 128, G_TMEM = 136
+enum : uint32_t {  // mbarriers, 8 bytes each
+  G_QK = 0, G_VO = 8, G_RH = 16, G_RL = 24, G_SH = 32, G_SL = 40,               // loaded
+  G_SC = 48, G_XR = 56, G_DV = 64, G_DK = 72, G_DQ = 80,                        // products done
+  G_P = 88, G_ACCFREE = 96, G_ENDFREE = 104, G_DOTS = 112,                      // epilogues' warps
+  G_RHREAD = 120, G_RLREAD = 128, G_SREAD = 136,                                // <S, R>'s warps
+  G_PAFREE = 144, G_KFREE = 152, G_QFREE = 160, G_FIN = 168, G_TMEM = 176       // stores have read
 };
 template <int DK, int DV>
 struct GradLayout {
@@ -875,12 +879,12 @@ struct GradLayout {
   static constexpr uint32_t PA_OFF = O_OFF + VB * kBlk, PB_OFF = PA_OFF + 2 * kBlk, X_OFF = PB_OFF + 2 * kBlk;
   static constexpr uint32_t END = X_OFF + STATE;
   static constexpr uint32_t SUF_OFF = END;  // suf[128], block products [4]
-  static constexpr uint32_t THR_OFF = SUF_OFF + 132 * 4;                 // <S, R> of 8 warps, gamma
-  static constexpr uint32_t BAR_OFF = (THR_OFF + 9 * 4 + 7) / 8 * 8;
-  static constexpr uint32_t BYTES = BAR_OFF + 152;
+  static constexpr uint32_t THR_OFF = SUF_OFF + 132 * 4;  // [2]: <S, R> of 8 warps, gamma
+  static constexpr uint32_t BAR_OFF = (THR_OFF + 18 * 4 + 7) / 8 * 8;
+  static constexpr uint32_t BYTES = BAR_OFF + 184;
   static constexpr uint32_t ALLOC = BYTES + 1024;
-  // the rows' sums at the end, over dO: F[2][128], e[2][128], column sums [4][128]
-  static constexpr uint32_t FSUM = O_OFF, ESUM = FSUM + 1024, CSUM = ESUM + 1024;
+  // the rows' sums at the end, over B: F[2][128], e[2][128], column sums [4][128]
+  static constexpr uint32_t FSUM = PB_OFF, ESUM = FSUM + 1024, CSUM = ESUM + 1024;
   static_assert(ALLOC <= 232448, "shared memory budget");
   static_assert(STATE <= VB * kBlk && STATE <= 2 * kBlk, "the states' places");
   static_assert(END % 1024 == 0, "128-byte swizzle atoms stay aligned");
@@ -945,25 +949,25 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                       const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmR,
                       const __grid_constant__ CUtensorMap tmDQ, const __grid_constant__ CUtensorMap tmDK,
                       const __grid_constant__ CUtensorMap tmDV, const float* alpha_all, float* dlog_alpha, int T,
-                      unsigned int* status) {
+                      int tasks, unsigned int* status) {
   using L = GradLayout<DK, DV>;
   constexpr int KB = L::KB, VB = L::VB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = warp_uniform(smem_u32(sm));
   const int tid = threadIdx.x, lane = tid & 31, warp = (int)warp_uniform((uint32_t)tid >> 5), w = warp & 3;
-  const int nch = (T + C - 1) / C, bh = blockIdx.x / nch, c = blockIdx.x % nch, t0 = c * C;
+  const int nch = (T + C - 1) / C;
   const uint32_t bar = sb + L::BAR_OFF;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::BAR_OFF + G_TMEM);
   float* suf = reinterpret_cast<float*>(sm + L::SUF_OFF);
   float* blk = suf + C;
-  float* thr = reinterpret_cast<float*>(sm + L::THR_OFF);
-  const float* alpha = GATED ? alpha_all + (size_t)bh * T : nullptr;
+  float* thr_all = reinterpret_cast<float*>(sm + L::THR_OFF);
 
   if (tid == 0) {
-    for (uint32_t b : {G_QK, G_VO, G_RH, G_RL, G_SH, G_SL, G_SC, G_DV, G_XR, G_DK, G_DQ, G_FIN})
-      mbar_init(bar + b, 1);
-    for (uint32_t b : {G_P, G_ACCFREE, G_RHREAD, G_RLREAD, G_DOTS}) mbar_init(bar + b, 8);  // one arrival per warp
+    for (uint32_t b = G_QK; b <= G_FIN; b += 8) {
+      const bool warps = (b >= G_P && b <= G_SREAD);
+      mbar_init(bar + b, warps ? 8 : 1);  // one arrival per warp
+    }
     fence_mbar_init();
   }
   if (warp == kWarpMma) {
@@ -975,7 +979,20 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   tc_fence_after();
   const uint32_t tmem = warp_uniform(*tmem_slot);
   unsigned int* const wc = status;
-  auto wait = [&](uint32_t b) { return wait_bar(bar + b, 0, wc); };
+  // a role's own chunk: its number among the CTA's, and its place
+  int it = 0, bh = 0, t0 = 0, task = blockIdx.x;
+  auto begin = [&]() {
+    if (task >= tasks) return false;
+    bh = task / nch;
+    t0 = (task - bh * nch) * C;
+    return true;
+  };
+  auto next = [&]() {
+    task += gridDim.x;
+    ++it;
+  };
+  auto wait = [&](uint32_t b) { return wait_bar(bar + b, it & 1, wc); };
+  auto wait_before = [&](uint32_t b) { return it == 0 || wait_bar(bar + b, (it - 1) & 1, wc); };
   auto wait_all = [&](uint32_t b) { return __all_sync(0xffffffffu, wait(b)) != 0; };
   auto arrive = [&](uint32_t b) {
     __syncwarp();
@@ -984,9 +1001,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 
   if (warp == kWarpTma) {
     if (lane == 0) {
-      const int at = (bh * nch + c) * 2;
       uint32_t got[6];
-      int n = 0;
+      int n = 0, at = 0;
       auto expect = [&](uint32_t b, uint32_t bytes) {
         mbar_expect_tx(bar + b, bytes);
         got[n++] = b;
@@ -996,26 +1012,61 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
         for (int i = 0; i < VB; ++i) tma_load_3d(sb + to + i * L::SBLK, m, bar + b, 64 * i, 0, z);
       };
-      expect(G_QK, 2 * KB * kBlk);
-#pragma unroll
-      for (int i = 0; i < KB; ++i) {
-        tma_load_3d(sb + L::Q_OFF + i * kBlk, &tmQ, bar + G_QK, 64 * i, t0, bh);
-        tma_load_3d(sb + L::K_OFF + i * kBlk, &tmK, bar + G_QK, 64 * i, t0, bh);
-      }
-      expect(G_VO, 2 * VB * kBlk);
-#pragma unroll
-      for (int i = 0; i < VB; ++i) {
-        tma_load_3d(sb + L::O_OFF + i * kBlk, &tmO, bar + G_VO, 64 * i, t0, bh);
-        tma_load_3d(sb + L::V_OFF + i * kBlk, &tmV, bar + G_VO, 64 * i, t0, bh);
-      }
-      state(G_RH, &tmR, L::X_OFF, at);
-      if (GATED) state(G_RL, &tmR, L::PA_OFF, at + 1);
-      if (wait(G_XR)) {  // the products with R (and V) have run
+      auto rows = [&](uint32_t b, const CUtensorMap* m, uint32_t to, int blocks) {
+        for (int i = 0; i < blocks; ++i) tma_load_3d(sb + to + i * kBlk, m, bar + b, 64 * i, t0, bh);
+      };
+      bool ok = true;
+      for (; ok && begin(); next()) {
+        at = 2 * task;
+        // the chunk before has come to its end with dO, V, X (its loads have landed, too) ...
+        ok = wait_before(G_DQ) && (!GATED || wait_before(G_SREAD));
+        if (!ok) break;
+        n = 0;
+        expect(G_VO, 2 * VB * kBlk);
+        rows(G_VO, &tmO, L::O_OFF, VB);
+        rows(G_VO, &tmV, L::V_OFF, VB);
+        state(G_RH, &tmR, L::X_OFF, at);
+        if (GATED) {  // ... with A's place, and its stores with K and Q
+          ok = wait_before(G_PAFREE);
+          if (!ok) break;
+          state(G_RL, &tmR, L::PA_OFF, at + 1);
+        }
+        ok = wait_before(G_KFREE) && wait_before(G_QFREE);
+        if (!ok) break;
+        expect(G_QK, 2 * KB * kBlk);
+        rows(G_QK, &tmK, L::K_OFF, KB);
+        rows(G_QK, &tmQ, L::Q_OFF, KB);
+        ok = wait(G_XR);  // the products with R (and V) have run
+        if (!ok) break;
         if (GATED) state(G_SL, &tmS, L::V_OFF, at + 1);
-        if (!GATED || wait(G_RHREAD)) state(G_SH, &tmS, L::X_OFF, at);
+        ok = !GATED || wait(G_RHREAD);
+        if (!ok) break;
+        state(G_SH, &tmS, L::X_OFF, at);
+        // The SMs run through their chunks at one pace, so their loads and stores
+        // come in bursts with nothing in between: the next chunk's tiles go to L2
+        // while the epilogues work on this one.
+        const int ahead = task + (int)gridDim.x;
+        if (ahead < tasks) {
+          const int nbh = ahead / nch, nt0 = (ahead - nbh * nch) * C;
+#pragma unroll 1
+          for (int i = 0; i < VB; ++i) {
+            prefetch_l2_3d(&tmO, 64 * i, nt0, nbh);
+            prefetch_l2_3d(&tmV, 64 * i, nt0, nbh);
+            for (int lo = 0; lo < (GATED ? 2 : 1); ++lo) {
+              prefetch_l2_3d(&tmR, 64 * i, 0, 2 * ahead + lo);
+              prefetch_l2_3d(&tmS, 64 * i, 0, 2 * ahead + lo);
+            }
+          }
+#pragma unroll 1
+          for (int i = 0; i < KB; ++i) {
+            prefetch_l2_3d(&tmK, 64 * i, nt0, nbh);
+            prefetch_l2_3d(&tmQ, 64 * i, nt0, nbh);
+          }
+        }
       }
-      // never leave with copies in flight
-      for (int i = 0; i < n; ++i) (void)wait_bar(bar + got[i], 0, wc);
+      // never leave with copies in flight: those of the last chunk
+      if (ok && it > 0) --it;
+      for (int i = 0; i < n; ++i) (void)wait(got[i]);
     }
   } else if (warp == kWarpMma) {
     // A: K-major tile of 64-column blocks `ab` apart; B: K-major blocks `bb` apart
@@ -1044,59 +1095,50 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       for (int ks = 0; ks < C / 16; ++ks)
         mma_bf16_ss_elect(tmem + d, desc_step(da, ks * 2048), desc_step(db, ks * 2048), id, ks > 0);
     };
-    bool ok = wait_all(G_QK);
-    if (ok) {
+    bool ok = true;
+    for (; ok && begin(); next()) {
+      // the epilogues of the chunk before have read the accumulators
+      ok = __all_sync(0xffffffffu, wait_before(G_ENDFREE)) && wait_all(G_VO) && wait_all(G_RH);
+      if (!ok) break;
       tc_fence_after();
-      kk(TG_A, L::Q_OFF, kBlk, L::K_OFF, kBlk, DK, 128, 0);  // Q K^T
-      ok = wait_all(G_VO);
-    }
-    if (ok) {
-      tc_fence_after();
-      kk(TG_B, L::O_OFF, kBlk, L::V_OFF, kBlk, DV, 128, 0);  // dO V^T
-      mma_commit_elect(bar + G_SC);
-      ok = wait_all(G_RH);
-    }
-    if (ok) {
-      tc_fence_after();
-      kn(TG_D, L::K_OFF, L::X_OFF, L::SBLK, DK, DV);           // K R
       kk(TG_C, L::V_OFF, kBlk, L::X_OFF, L::SBLK, DV, DK, 0);  // V R^T, hi
       if (GATED) {
         ok = wait_all(G_RL);
-        if (ok) {
-          tc_fence_after();
-          kk(TG_C, L::V_OFF, kBlk, L::PA_OFF, L::SBLK, DV, DK, 1);  // V R^T, lo
-        }
+        if (!ok) break;
+        tc_fence_after();
+        kk(TG_C, L::V_OFF, kBlk, L::PA_OFF, L::SBLK, DV, DK, 1);  // V R^T, lo
       }
-    }
-    if (ok) {
+      ok = wait_all(G_QK);
+      if (!ok) break;
+      tc_fence_after();
+      kk(TG_A, L::Q_OFF, kBlk, L::K_OFF, kBlk, DK, 128, 0);  // Q K^T
+      kk(TG_B, L::O_OFF, kBlk, L::V_OFF, kBlk, DV, 128, 0);  // dO V^T
+      mma_commit_elect(bar + G_SC);
+      kn(TG_D, L::K_OFF, L::X_OFF, L::SBLK, DK, DV);  // K R
       mma_commit_elect(bar + G_XR);
       ok = wait_all(G_P);
-    }
-    if (ok) {
+      if (!ok) break;
       tc_fence_after();
       nn(TG_A, L::PA_OFF, L::O_OFF, DV);  // A^T dO
       mma_commit_elect(bar + G_DV);
       nn(TG_B, L::PB_OFF, L::Q_OFF, DK);  // B^T Q
       ok = wait_all(G_ACCFREE);           // dV's parts have been read
-    }
-    if (ok) {
+      if (!ok) break;
       tc_fence_after();
       kn(TG_A, L::PB_OFF, L::K_OFF, kBlk, C, DK);  // B K
       mma_commit_elect(bar + G_DK);                // with it, K and Q are free to be staged over
       ok = wait_all(G_SH);
-    }
-    if (ok) {
+      if (!ok) break;
       tc_fence_after();
       kk(TG_D, L::O_OFF, kBlk, L::X_OFF, L::SBLK, DV, DK, 0);  // dO S^T, hi
       if (GATED) {
         ok = wait_all(G_SL);
-        if (ok) {
-          tc_fence_after();
-          kk(TG_D, L::O_OFF, kBlk, L::V_OFF, L::SBLK, DV, DK, 1);  // dO S^T, lo
-        }
+        if (!ok) break;
+        tc_fence_after();
+        kk(TG_D, L::O_OFF, kBlk, L::V_OFF, L::SBLK, DV, DK, 1);  // dO S^T, lo
       }
+      mma_commit_elect(bar + G_DQ);
     }
-    if (ok) mma_commit_elect(bar + G_DQ);
     tc_fence_after();  // no MMA may outlive TMEM
     mma_commit_elect(bar + G_FIN);
     (void)wait_bar(bar + G_FIN, 0, wc);
@@ -1105,91 +1147,6 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     const int row = 32 * w + lane, half = (warp - 4) >> 2;
     const bool leader = warp == 4 && lane == 0;
     const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
-    float a = 1.f, pre = 1.f, into = 1.f, out = 1.f;
-    if (GATED) {
-      float al[4];
-      load_alpha(alpha, T, c, al);
-      into = decay_into(al, w);
-      out = decay_out(al, w);
-      a = w == 0 ? al[0] : w == 1 ? al[1] : w == 2 ? al[2] : al[3];
-      pre = prefix_product(a);
-      if (half == 0) {
-        suf[row] = suffix_product(a);
-        if (lane == 31) blk[w] = pre;
-        const float gamma = decay_chunk(al);
-        if (leader) thr[8] = gamma;
-      }
-    }
-    // ---- A, B and M's sums ----
-    float fsum = 0.f, esum = 0.f, csum[4] = {0.f, 0.f, 0.f, 0.f};
-    bool ok = named_bar_and(kBarE, 256, wait(G_SC));
-    if (ok) {
-      tc_fence_after();
-      float run = 0.f;
-      bool room = false;  // A's place is free of R lo
-#pragma unroll 1
-      for (int pc = 3; pc >= 0; --pc) {  // 16 columns at a time, the right ones first
-        const int c0 = 64 * half + 16 * pc, cb = c0 >> 5;
-        uint32_t pa[8], pb[8];
-        if (cb <= w) {
-          uint32_t x[16], y[16];
-          float m[16];
-          tmem_ld16(lanes + TG_A + c0, x);
-          tmem_ld16(lanes + TG_B + c0, y);
-          if (GATED && cb < w) {
-            float mid = pre;
-            if (cb + 1 < w) mid *= blk[w - 1];
-            if (cb + 2 < w) mid *= blk[w - 2];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) m[j] = mid * suf[c0 + j];
-          } else {  // the product of alpha over (column, row], zero right of the diagonal
-            const int b0 = c0 & 31;
-#pragma unroll
-            for (int j = 15; j >= 0; --j) {
-              if (GATED) {
-                const float t = __shfl_sync(0xffffffffu, a, b0 + j + 1);
-                run = b0 + j == lane ? 1.f : run * t;
-                m[j] = run;
-              } else {
-                m[j] = cb < w || b0 + j <= lane ? 1.f : 0.f;
-              }
-            }
-          }
-          tmem_wait_ld();
-          const int diag = cb == w ? lane - (c0 & 31) : -1;  // the diagonal's column of the piece
-#pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const float s0 = __uint_as_float(x[j]), s1 = __uint_as_float(x[j + 1]);
-            const float b0 = __uint_as_float(y[j]) * m[j], b1 = __uint_as_float(y[j + 1]) * m[j + 1];
-            pa[j / 2] = pack2_bf16(s0 * m[j], s1 * m[j + 1]);
-            pb[j / 2] = pack2_bf16(b0, b1);
-            m[j] = j == diag ? 0.f : s0 * b0;
-            m[j + 1] = j + 1 == diag ? 0.f : s1 * b1;
-            if (GATED) fsum += m[j] + m[j + 1];
-          }
-          if (GATED) {
-            const float v = fold16(m);
-            csum[0] = pc == 0 ? v : csum[0];
-            csum[1] = pc == 1 ? v : csum[1];
-            csum[2] = pc == 2 ? v : csum[2];
-            csum[3] = pc == 3 ? v : csum[3];
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) pa[i] = pb[i] = 0;
-        }
-        if (GATED && !room) room = wait(G_XR) && wait(G_RLREAD);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t at = (uint32_t)half * kBlk + sw128_off(row, 2 * pc + h);
-          *reinterpret_cast<uint4*>(sm + L::PA_OFF + at) = make_uint4(pa[4 * h], pa[4 * h + 1], pa[4 * h + 2], pa[4 * h + 3]);
-          *reinterpret_cast<uint4*>(sm + L::PB_OFF + at) = make_uint4(pb[4 * h], pb[4 * h + 1], pb[4 * h + 2], pb[4 * h + 3]);
-        }
-      }
-      tc_fence_before();
-      fence_proxy_async_smem();
-      arrive(G_P);
-    }
     // the eight warps meet at every staged tile, so they leave together
     auto store = [&](const CUtensorMap* m, uint32_t from, int blocks) {
       fence_proxy_async_smem();
@@ -1200,113 +1157,222 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       }
       __syncwarp();
     };
-    ok = named_bar_and(kBarE, 256, ok && wait(G_DV));
-    if (ok) {
-      tc_fence_after();
-      grad_row<DV / 2, false>(lanes + TG_D, lanes + TG_A, out, nullptr, sm + L::PA_OFF, row, half * (DV / 2));
-      tc_fence_before();
-      arrive(G_ACCFREE);
-      store(&tmDV, L::PA_OFF, VB);
-      ok = named_bar_and(kBarE, 256, wait(G_DK));
-    }
-    if (ok) {
-      tc_fence_after();
-      esum = grad_row<DK / 2, GATED>(lanes + TG_C, lanes + TG_B, out, sm + L::K_OFF, sm + L::K_OFF, row, half * (DK / 2));
-      store(&tmDK, L::K_OFF, KB);
-      ok = named_bar_and(kBarE, 256, wait(G_DQ));
-    }
-    if (ok) {
-      tc_fence_after();
-      fsum += grad_row<DK / 2, GATED>(lanes + TG_D, lanes + TG_A, into, sm + L::Q_OFF, sm + L::Q_OFF, row, half * (DK / 2));
-      if (GATED) {  // dO has been read: its place takes the sums
-        reinterpret_cast<float*>(sm + L::FSUM)[half * C + row] = fsum;
-        reinterpret_cast<float*>(sm + L::ESUM)[half * C + row] = esum;
-        if (lane < 16) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            reinterpret_cast<float*>(sm + L::CSUM)[w * C + 64 * half + 16 * i + fold16_col(lane)] = csum[i];
+    bool ok = true;
+    for (; ok && begin(); next()) {
+      float a = 1.f, pre = 1.f, into = 1.f, out = 1.f;
+      if (GATED) {
+        float al[4];
+        load_alpha(alpha_all + (size_t)bh * T, T, t0 / C, al);
+        into = decay_into(al, w);
+        out = decay_out(al, w);
+        a = w == 0 ? al[0] : w == 1 ? al[1] : w == 2 ? al[2] : al[3];
+        pre = prefix_product(a);
+        if (half == 0) {
+          suf[row] = suffix_product(a);
+          if (lane == 31) blk[w] = pre;
+          const float gamma = decay_chunk(al);
+          if (leader) thr_all[9 * (it & 1) + 8] = gamma;
         }
-        arrive(G_DOTS);
       }
-      store(&tmDQ, L::Q_OFF, KB);
+      // ---- A, B and M's sums ----
+      float fsum = 0.f, esum = 0.f, csum[4] = {0.f, 0.f, 0.f, 0.f};
+      ok = named_bar_and(kBarE, 256, wait(G_SC));
+      if (ok) {
+        tc_fence_after();
+        float run = 0.f;
+        bool room = false;  // A's place is free of R lo
+#pragma unroll 1
+        for (int pc = 3; pc >= 0; --pc) {  // 16 columns at a time, the right ones first
+          const int c0 = 64 * half + 16 * pc, cb = c0 >> 5;
+          uint32_t pa[8], pb[8];
+          if (cb <= w) {
+            uint32_t x[16], y[16];
+            float m[16];
+            tmem_ld16(lanes + TG_A + c0, x);
+            tmem_ld16(lanes + TG_B + c0, y);
+            if (GATED && cb < w) {
+              float mid = pre;
+              if (cb + 1 < w) mid *= blk[w - 1];
+              if (cb + 2 < w) mid *= blk[w - 2];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) m[j] = mid * suf[c0 + j];
+            } else {  // the product of alpha over (column, row], zero right of the diagonal
+              const int b0 = c0 & 31;
+#pragma unroll
+              for (int j = 15; j >= 0; --j) {
+                if (GATED) {
+                  const float t = __shfl_sync(0xffffffffu, a, b0 + j + 1);
+                  run = b0 + j == lane ? 1.f : run * t;
+                  m[j] = run;
+                } else {
+                  m[j] = cb < w || b0 + j <= lane ? 1.f : 0.f;
+                }
+              }
+            }
+            tmem_wait_ld();
+            const int diag = cb == w ? lane - (c0 & 31) : -1;  // the diagonal's column of the piece
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              const float s0 = __uint_as_float(x[j]), s1 = __uint_as_float(x[j + 1]);
+              const float b0 = __uint_as_float(y[j]) * m[j], b1 = __uint_as_float(y[j + 1]) * m[j + 1];
+              pa[j / 2] = pack2_bf16(s0 * m[j], s1 * m[j + 1]);
+              pb[j / 2] = pack2_bf16(b0, b1);
+              m[j] = j == diag ? 0.f : s0 * b0;
+              m[j + 1] = j + 1 == diag ? 0.f : s1 * b1;
+              if (GATED) fsum += m[j] + m[j + 1];
+            }
+            if (GATED) {
+              const float v = fold16(m);
+              csum[0] = pc == 0 ? v : csum[0];
+              csum[1] = pc == 1 ? v : csum[1];
+              csum[2] = pc == 2 ? v : csum[2];
+              csum[3] = pc == 3 ? v : csum[3];
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) pa[i] = pb[i] = 0;
+          }
+          if (GATED && !room) room = wait(G_XR) && wait(G_RLREAD);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t at = (uint32_t)half * kBlk + sw128_off(row, 2 * pc + h);
+            *reinterpret_cast<uint4*>(sm + L::PA_OFF + at) = make_uint4(pa[4 * h], pa[4 * h + 1], pa[4 * h + 2], pa[4 * h + 3]);
+            *reinterpret_cast<uint4*>(sm + L::PB_OFF + at) = make_uint4(pb[4 * h], pb[4 * h + 1], pb[4 * h + 2], pb[4 * h + 3]);
+          }
+        }
+        tc_fence_before();
+        fence_proxy_async_smem();
+        arrive(G_P);
+      }
+      ok = named_bar_and(kBarE, 256, ok && wait(G_DV));
+      if (ok) {
+        tc_fence_after();
+        grad_row<DV / 2, false>(lanes + TG_D, lanes + TG_A, out, nullptr, sm + L::PA_OFF, row, half * (DV / 2));
+        tc_fence_before();
+        arrive(G_ACCFREE);
+        store(&tmDV, L::PA_OFF, VB);
+        ok = named_bar_and(kBarE, 256, wait(G_DK));
+      }
+      if (ok) {
+        tc_fence_after();
+        esum = grad_row<DK / 2, GATED>(lanes + TG_C, lanes + TG_B, out, sm + L::K_OFF, sm + L::K_OFF, row, half * (DK / 2));
+        store(&tmDK, L::K_OFF, KB);
+        if (leader) {
+          bulk_wait_group_read<1>();
+          mbar_arrive(bar + G_PAFREE);
+        }
+        __syncwarp();
+        ok = named_bar_and(kBarE, 256, wait(G_DQ));
+      }
+      if (ok) {
+        tc_fence_after();
+        fsum += grad_row<DK / 2, GATED>(lanes + TG_D, lanes + TG_A, into, sm + L::Q_OFF, sm + L::Q_OFF, row, half * (DK / 2));
+        tc_fence_before();
+        arrive(G_ENDFREE);
+        if (GATED) {  // B has been read: its place takes the sums
+          reinterpret_cast<float*>(sm + L::FSUM)[half * C + row] = fsum;
+          reinterpret_cast<float*>(sm + L::ESUM)[half * C + row] = esum;
+          if (lane < 16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              reinterpret_cast<float*>(sm + L::CSUM)[w * C + 64 * half + 16 * i + fold16_col(lane)] = csum[i];
+          }
+          arrive(G_DOTS);
+        }
+        store(&tmDQ, L::Q_OFF, KB);
+        if (leader) {
+          bulk_wait_group_read<1>();
+          mbar_arrive(bar + G_KFREE);
+          bulk_wait_group_read<0>();
+          mbar_arrive(bar + G_QFREE);
+        }
+        __syncwarp();
+      }
     }
     if (leader) bulk_wait_group_all();
   } else if (GATED && warp >= 12) {
     // ------------------------------------------------- <S, R> and the sums --
     constexpr int NP = (int)(L::STATE / 16 / 256);  // 16-byte pieces of a state tile to a thread
     const int i0 = tid - 12 * 32;
-    float r[NP][8], dot = 0.f;
+    float r[NP][8];
     auto piece = [&](uint32_t tile, int i, float (&x)[8]) {
       unpack_bf16x8(*reinterpret_cast<const uint4*>(sm + tile + 16 * (i0 + 256 * i)), x);
     };
-    bool ok = wait_all(G_RH);
-    if (ok) {
+    bool ok = true;
+    for (; ok && begin(); next()) {
+      float* thr = thr_all + 9 * (it & 1);
+      const float* alpha = alpha_all + (size_t)bh * T;
+      float dot = 0.f;
+      ok = wait_all(G_RH);
+      if (ok) {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) piece(L::X_OFF, i, r[i]);
-      arrive(G_RHREAD);
-      ok = wait_all(G_RL);
-    }
-    if (ok) {
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        float x[8];
-        piece(L::PA_OFF, i, x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r[i][e] += x[e];
+        for (int i = 0; i < NP; ++i) piece(L::X_OFF, i, r[i]);
+        arrive(G_RHREAD);
+        ok = wait_all(G_RL);
       }
-      arrive(G_RLREAD);
-    }
-#pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      ok = ok && wait_all(part ? G_SL : G_SH);
       if (ok) {
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           float x[8];
-          piece(part ? L::V_OFF : L::X_OFF, i, x);
+          piece(L::PA_OFF, i, x);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dot = fmaf(x[e], r[i][e], dot);
+          for (int e = 0; e < 8; ++e) r[i][e] += x[e];
+        }
+        arrive(G_RLREAD);
+      }
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        ok = ok && wait_all(part ? G_SL : G_SH);
+        if (ok) {
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            float x[8];
+            piece(part ? L::V_OFF : L::X_OFF, i, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot = fmaf(x[e], r[i][e], dot);
+          }
         }
       }
-    }
+      if (ok) arrive(G_SREAD);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if (lane == 0) thr[warp - 12] = dot;
-    ok = named_bar_and(kBarT, 256, ok && wait(G_DOTS));
-    if (ok && dlog_alpha && warp == 12) {  // four tokens to a lane
-      float sr = 0.f;
+      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if (lane == 0) thr[warp - 12] = dot;
+      ok = named_bar_and(kBarT, 256, ok && wait(G_DOTS));
+      if (ok && dlog_alpha && warp == 12) {  // four tokens to a lane
+        float sr = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sr += thr[i];
-      sr *= thr[8];
-      const float* F = reinterpret_cast<const float*>(sm + L::FSUM);
-      const float* E = reinterpret_cast<const float*>(sm + L::ESUM);
-      const float* S = reinterpret_cast<const float*>(sm + L::CSUM);
-      float f[4], e[4];
+        for (int i = 0; i < 8; ++i) sr += thr[i];
+        sr *= thr[8];
+        const float* F = reinterpret_cast<const float*>(sm + L::FSUM);
+        const float* E = reinterpret_cast<const float*>(sm + L::ESUM);
+        const float* S = reinterpret_cast<const float*>(sm + L::CSUM);
+        float f[4], e[4];
 #pragma unroll
-      for (int k = 3; k >= 0; --k) {  // suffix sums of the lane's own tokens
-        const int t = 4 * lane + k;
-        f[k] = F[t] + F[C + t] - (S[t] + S[C + t] + S[2 * C + t] + S[3 * C + t]) + (k < 3 ? f[k + 1] : 0.f);
-      }
+        for (int k = 3; k >= 0; --k) {  // suffix sums of the lane's own tokens
+          const int t = 4 * lane + k;
+          f[k] = F[t] + F[C + t] - (S[t] + S[C + t] + S[2 * C + t] + S[3 * C + t]) + (k < 3 ? f[k + 1] : 0.f);
+        }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) e[k] = E[4 * lane + k] + E[C + 4 * lane + k] + (k > 0 ? e[k - 1] : 0.f);
-      float suff = f[0], pref = e[3];
+        for (int k = 0; k < 4; ++k) e[k] = E[4 * lane + k] + E[C + 4 * lane + k] + (k > 0 ? e[k - 1] : 0.f);
+        float suff = f[0], pref = e[3];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float x = __shfl_down_sync(0xffffffffu, suff, o), y = __shfl_up_sync(0xffffffffu, pref, o);
-        if (lane + o < 32) suff += x;
-        if (lane >= o) pref += y;
-      }
-      suff = __shfl_down_sync(0xffffffffu, suff, 1);  // tokens of later lanes
-      pref = __shfl_up_sync(0xffffffffu, pref, 1);    // of earlier ones
-      if (lane == 31) suff = 0.f;
-      if (lane == 0) pref = 0.f;
+        for (int o = 1; o < 32; o <<= 1) {
+          const float x = __shfl_down_sync(0xffffffffu, suff, o), y = __shfl_up_sync(0xffffffffu, pref, o);
+          if (lane + o < 32) suff += x;
+          if (lane >= o) pref += y;
+        }
+        suff = __shfl_down_sync(0xffffffffu, suff, 1);  // tokens of later lanes
+        pref = __shfl_up_sync(0xffffffffu, pref, 1);    // of earlier ones
+        if (lane == 31) suff = 0.f;
+        if (lane == 0) pref = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int t = t0 + 4 * lane + k;
-        // no path crosses a wipe: its derivative is 0, not the sums' rounding
-        if (t < T)
-          dlog_alpha[(size_t)bh * T + t] =
-              alpha[t] == 0.f ? 0.f : f[k] + suff + pref + (k > 0 ? e[k - 1] : 0.f) + sr;
+        for (int k = 0; k < 4; ++k) {
+          const int t = t0 + 4 * lane + k;
+          // no path crosses a wipe: its derivative is 0, not the sums' rounding
+          if (t < T)
+            dlog_alpha[(size_t)bh * T + t] =
+                alpha[t] == 0.f ? 0.f : f[k] + suff + pref + (k > 0 ? e[k - 1] : 0.f) + sr;
+        }
       }
     }
   }
@@ -1404,8 +1470,9 @@ cudaError_t launch_grad(const GatedProblem& p, const void* S, const void* R, cud
   constexpr int smem = (int)GradLayout<DK, DV>::ALLOC;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)((size_t)BH * nch), GATED ? kGradThreads : kGradPlain, smem, st>>>(
-      mq, mk, mv, mo, ms, mr, mdq, mdk, mdv, p.alpha, p.dlog_alpha, p.T, p.status);
+  const int tasks = BH * nch;
+  kern<<<p.sms > 0 && p.sms < tasks ? p.sms : tasks, GATED ? kGradThreads : kGradPlain, smem, st>>>(
+      mq, mk, mv, mo, ms, mr, mdq, mdk, mdv, p.alpha, p.dlog_alpha, p.T, tasks, p.status);
   return cudaGetLastError();
 }
 

@@ -153,6 +153,7 @@ struct GatedProblem {
   int bf16;
   unsigned int* status;
   int G, seg_chunks;   // bf16: segments of the sequence and their chunks (gated_segments)
+  int sms;             // bf16 gradient: SMs of the device
 };
 // Tokens of a chunk of the CUDA-core kernels (the float32 path).
 constexpr int kGatedSimtChunk = 32;
