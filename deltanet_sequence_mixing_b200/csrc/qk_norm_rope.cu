@@ -15,7 +15,10 @@
 // Bound by HBM: one read and one write of every row (two reads in the
 // gradient).  A row belongs to D / 16 lanes, and each lane holds two 16-byte
 // pieces that form whole pairs (pieces l and l + rot/16 of the rotated half, or
-// neighbours), so the turn needs no exchange and the norm three shuffles.
+// neighbours), so the turn needs no exchange and the norm three shuffles.  A
+// lane's columns are the same in every row: the weights (and in the gradient
+// their sums) stay in registers, one half of the grid taking the queries and the
+// other the keys.
 // Angles: position * inv_freq in float64, in turns, its whole part dropped,
 // then sine and cosine in float32: exact to float32 at any position.  A CTA
 // computes them once for a token and uses them for all of its heads.
@@ -59,44 +62,38 @@ __device__ __forceinline__ void pieces_of(int l, int rot, int interleaved, int& 
   }
 }
 
-// The turn by +angle (way = 1) or -angle (way = -1) of a lane's 16 values.
+// The turn by +angle (way = 1) or -angle (way = -1) of a lane's 16 values: the
+// cosines and sines of its 8 pairs stand in a row.
 template <bool INTER>
-__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float2* cs, int l, float way) {
-  if (INTER) {
+__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float* cs, const float* sn, float way) {
+  float c[8], s[8];
+  load_piece(cs, c);
+  load_piece(sn, s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 u = cs[8 * l + i], w = cs[8 * l + 4 + i];
-      const float x0 = a[2 * i], x1 = a[2 * i + 1], y0 = b[2 * i], y1 = b[2 * i + 1];
-      a[2 * i] = x0 * u.x - way * x1 * u.y;
-      a[2 * i + 1] = x1 * u.x + way * x0 * u.y;
-      b[2 * i] = y0 * w.x - way * y1 * w.y;
-      b[2 * i + 1] = y1 * w.x + way * y0 * w.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 u = cs[8 * l + i];
-      const float x0 = a[i], x1 = b[i];
-      a[i] = x0 * u.x - way * x1 * u.y;
-      b[i] = x1 * u.x + way * x0 * u.y;
-    }
+  for (int i = 0; i < 8; ++i) {
+    float& x = INTER ? (i < 4 ? a[2 * (i & 3)] : b[2 * (i & 3)]) : a[i];
+    float& y = INTER ? (i < 4 ? a[2 * (i & 3) + 1] : b[2 * (i & 3) + 1]) : b[i];
+    const float x0 = x, ws = way * s[i];
+    x = x0 * c[i] - y * ws;
+    y = y * c[i] + x0 * ws;
   }
 }
 
 __device__ __forceinline__ float sigmoid_f(float x) { return 1.f / (1.f + __expf(-x)); }
 
-// cos and sin of the angles of tokens [n0, n0 + nt) (flat over B x T).
-__device__ __forceinline__ void fill_turns(const QkProblem& p, long long n0, int nt, float2* cs) {
+// cos and sin of the angles of tokens [n0, n0 + nt) (flat over B x T): `half`
+// cosines, then as many sines, for each token.
+__device__ __forceinline__ void fill_turns(const QkProblem& p, int n0, int nt, float* turns) {
   const int half = p.rot / 2;
   for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-    const long long n = n0 + i / half;
-    const long long b = n / p.T, t = n % p.T;
+    const int tok = i / half, f = i - tok * half, b = (n0 + tok) / p.T, t = (n0 + tok) - b * p.T;
     const double pos = p.positions ? (double)p.positions[b * p.pos_stride_b + t] : (double)t;
-    double turns = pos * (double)p.inv_freq[i % half] * 0.15915494309189533576888;  // 1 / (2 pi)
-    turns -= rint(turns);
+    double x = pos * (double)p.inv_freq[f] * 0.15915494309189533576888;  // 1 / (2 pi)
+    x -= rint(x);
     float s, c;
-    sincospif(2.f * (float)turns, &s, &c);
-    cs[i] = make_float2(c, s);
+    sincospif(2.f * (float)x, &s, &c);
+    turns[2 * half * tok + f] = c;
+    turns[2 * half * tok + half + f] = s;
   }
 }
 
@@ -118,179 +115,197 @@ __device__ __forceinline__ float row_scale(const QkProblem& p, float ss, bool& f
   return rsqrtf(ss * (1.f / D) + p.eps);
 }
 
-struct Row {  // one row's place
-  bool live, is_k;
-  int h;
-  long long b, t;
+// One tensor of the two, as a CTA sees it.
+struct Side {
+  const void* x;
+  const void* g;       // gradient: the derivative by the output
+  const float* w;
+  void* out;
+  int H;
+  long long xb, xt, xh;  // strides of x
+  long long ob, ot, oh;  // gradient: of out
 };
-
-template <int D>
-__device__ __forceinline__ Row row_of(const QkProblem& p, long long n0, int nt, int i) {
-  const int heads = p.Hq + p.Hk;
-  Row r;
-  r.live = i < nt * heads;
-  const int tok = r.live ? i / heads : 0;
-  const int hh = r.live ? i - tok * heads : 0;
-  r.is_k = hh >= p.Hq;
-  r.h = r.is_k ? hh - p.Hq : hh;
-  r.b = (n0 + tok) / p.T;
-  r.t = (n0 + tok) - r.b * p.T;
-  return r;
+__device__ __forceinline__ Side side_of(const QkProblem& p, bool key) {
+  if (key) return Side{p.k, p.dk_in, p.k_weight, p.k_out, p.Hk, p.ks_b, p.ks_t, p.ks_h, p.dks_b, p.dks_t, p.dks_h};
+  return Side{p.q, p.dq_in, p.q_weight, p.q_out, p.Hq, p.qs_b, p.qs_t, p.qs_h, p.dqs_b, p.dqs_t, p.dqs_h};
 }
+
+// The rows of a tile of nt tokens with H heads, ROWS of them at a time: this
+// thread's token and head, stepped without a division.
+template <int ROWS>
+struct Walk {
+  int tok, h, dtok, dh, H;
+  __device__ Walk(int first, int heads) : H(heads) {
+    tok = first / heads;
+    h = first - tok * heads;
+    dtok = ROWS / heads;
+    dh = ROWS - dtok * heads;
+  }
+  __device__ void step() {
+    tok += dtok;
+    h += dh;
+    if (h >= H) {
+      h -= H;
+      ++tok;
+    }
+  }
+};
 
 template <typename TI, int D, bool INTER>
 __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkProblem p, int tokens) {
   constexpr int L = D / 16, ROWS = kThreads / L;
-  extern __shared__ float2 cs[];
-  const long long N = (long long)p.B * p.T, n0 = (long long)blockIdx.x * tokens;
-  const int nt = (int)(N - n0 < tokens ? N - n0 : tokens), heads = p.Hq + p.Hk, half = p.rot / 2;
+  extern __shared__ float turns[];
+  const Side s = side_of(p, blockIdx.y);
+  const int N = p.B * p.T, n0 = (int)blockIdx.x * tokens, nt = min(tokens, N - n0), half = p.rot / 2;
   const int l = threadIdx.x % L;
+  if (s.H == 0) return;
   int c0, c1;
   pieces_of(l, p.rot, INTER, c0, c1);
   const bool turned = l < p.rot / 16;
-  if (half) fill_turns(p, n0, nt, cs);
+  float wa[8], wb[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    wa[e] = s.w ? s.w[c0 + e] : 1.f;
+    wb[e] = s.w ? s.w[c1 + e] : 1.f;
+  }
+  if (half) fill_turns(p, n0, nt, turns);
   __syncthreads();
-  for (int i0 = 0; i0 < nt * heads; i0 += ROWS) {
-    const int i = i0 + threadIdx.x / L;
-    const Row r = row_of<D>(p, n0, nt, i);
-    const int tok = r.live ? i / heads : 0;
-    float a[8] = {}, b[8] = {};
-    if (r.live) {
-      const TI* x = r.is_k ? static_cast<const TI*>(p.k) + r.b * p.ks_b + r.t * p.ks_t + r.h * p.ks_h
-                           : static_cast<const TI*>(p.q) + r.b * p.qs_b + r.t * p.qs_t + r.h * p.qs_h;
-      load_piece(x + c0, a);
-      load_piece(x + c1, b);
+  Walk<ROWS> at(threadIdx.x / L, s.H);
+  for (int i0 = 0; i0 < nt * s.H; i0 += ROWS, at.step()) {
+    const bool live = at.tok < nt;
+    const int n = n0 + at.tok, b = n / p.T, t = n - b * p.T;
+    float x[8] = {}, y[8] = {};
+    if (live) {
+      const TI* in = static_cast<const TI*>(s.x) + b * s.xb + t * s.xt + at.h * s.xh;
+      load_piece(in + c0, x);
+      load_piece(in + c1, y);
     }
     float ss = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       if (p.silu) {
-        a[e] *= sigmoid_f(a[e]);
-        b[e] *= sigmoid_f(b[e]);
+        x[e] *= sigmoid_f(x[e]);
+        y[e] *= sigmoid_f(y[e]);
       }
-      ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
+      ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
     }
     ss = row_sum<D>(ss);
-    if (!r.live) continue;
+    if (!live) continue;
     bool floored;
     const float scale = row_scale<D>(p, ss, floored);
-    const float* w = r.is_k ? p.k_weight : p.q_weight;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      a[e] *= scale * (w ? w[c0 + e] : 1.f);
-      b[e] *= scale * (w ? w[c1 + e] : 1.f);
+      x[e] *= scale * wa[e];
+      y[e] *= scale * wb[e];
     }
-    if (turned) turn<INTER>(a, b, cs + tok * half, l, 1.f);
-    TI* o = static_cast<TI*>(r.is_k ? p.k_out : p.q_out) +
-            ((r.b * (r.is_k ? p.Hk : p.Hq) + r.h) * (long long)p.T + r.t) * D;
-    store_piece(o + c0, a);
-    store_piece(o + c1, b);
+    if (turned) turn<INTER>(x, y, turns + 2 * half * at.tok + 8 * l, turns + 2 * half * at.tok + half + 8 * l, 1.f);
+    TI* o = static_cast<TI*>(s.out) + (((long long)b * s.H + at.h) * p.T + t) * D;
+    store_piece(o + c0, x);
+    store_piece(o + c1, y);
   }
 }
 
 // Gradient.  CTAs walk the token tiles with a stride, so that the weights'
-// gradients stay in registers until the end; every CTA then leaves its two
-// rows of partial sums and a second kernel adds them in a fixed order.
+// gradients stay in registers until the end; every CTA then leaves its row of
+// partial sums and a second kernel adds them in a fixed order.
 template <typename TI, typename TG, int D, bool INTER>
 __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkProblem p, int tokens) {
   constexpr int L = D / 16, ROWS = kThreads / L;
-  extern __shared__ float2 cs[];
+  extern __shared__ float turns[];
   __shared__ float part[kThreads / 32][D];
-  const long long N = (long long)p.B * p.T;
-  const int heads = p.Hq + p.Hk, half = p.rot / 2;
+  const Side s = side_of(p, blockIdx.y);
+  const int N = p.B * p.T, half = p.rot / 2;
   const int l = threadIdx.x % L, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int c0, c1;
   pieces_of(l, p.rot, INTER, c0, c1);
   const bool turned = l < p.rot / 16;
-  float dw[2][16] = {};
-  for (long long n0 = (long long)blockIdx.x * tokens; n0 < N; n0 += (long long)gridDim.x * tokens) {
-    const int nt = (int)(N - n0 < tokens ? N - n0 : tokens);
+  float wa[8], wb[8], dwa[8] = {}, dwb[8] = {};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    wa[e] = s.w ? s.w[c0 + e] : 1.f;
+    wb[e] = s.w ? s.w[c1 + e] : 1.f;
+  }
+  for (long long first = (long long)blockIdx.x * tokens; s.H > 0 && first < N; first += (long long)gridDim.x * tokens) {
+    const int n0 = (int)first, nt = min(tokens, N - n0);
     __syncthreads();  // the turns of the tile before have been read
-    if (half) fill_turns(p, n0, nt, cs);
+    if (half) fill_turns(p, n0, nt, turns);
     __syncthreads();
-    for (int i0 = 0; i0 < nt * heads; i0 += ROWS) {
-      const int i = i0 + threadIdx.x / L;
-      const Row r = row_of<D>(p, n0, nt, i);
-      const int tok = r.live ? i / heads : 0;
-      const long long in = r.is_k ? r.b * p.ks_b + r.t * p.ks_t + r.h * p.ks_h
-                                  : r.b * p.qs_b + r.t * p.qs_t + r.h * p.qs_h;
-      float a[8] = {}, b[8] = {}, da[8] = {}, db[8] = {};
-      if (r.live) {
-        const TI* x = static_cast<const TI*>(r.is_k ? p.k : p.q) + in;
-        const TG* g = static_cast<const TG*>(r.is_k ? p.dk_in : p.dq_in) +
-                      ((r.b * (r.is_k ? p.Hk : p.Hq) + r.h) * (long long)p.T + r.t) * D;
-        load_piece(x + c0, a);
-        load_piece(x + c1, b);
-        load_piece(g + c0, da);
-        load_piece(g + c1, db);
-        if (turned) turn<INTER>(da, db, cs + tok * half, l, -1.f);
+    Walk<ROWS> at(threadIdx.x / L, s.H);
+    for (int i0 = 0; i0 < nt * s.H; i0 += ROWS, at.step()) {
+      const bool live = at.tok < nt;
+      const int n = n0 + at.tok, b = n / p.T, t = n - b * p.T;
+      float x[8] = {}, y[8] = {}, dx[8] = {}, dy[8] = {};
+      if (live) {
+        const TI* in = static_cast<const TI*>(s.x) + b * s.xb + t * s.xt + at.h * s.xh;
+        const TG* g = static_cast<const TG*>(s.g) + (((long long)b * s.H + at.h) * p.T + t) * D;
+        load_piece(in + c0, x);
+        load_piece(in + c1, y);
+        load_piece(g + c0, dx);
+        load_piece(g + c1, dy);
+        if (turned)
+          turn<INTER>(dx, dy, turns + 2 * half * at.tok + 8 * l, turns + 2 * half * at.tok + half + 8 * l, -1.f);
       }
-      float sa[8], sb[8], ss = 0.f;  // silu' where it applies
+      // z over x in place; silu' is formed again from x at the end
+      float ss = 0.f, zx[8], zy[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        sa[e] = sb[e] = 1.f;
-        if (p.silu) {
-          const float s0 = sigmoid_f(a[e]), s1 = sigmoid_f(b[e]);
-          sa[e] = s0 * fmaf(a[e], 1.f - s0, 1.f);
-          sb[e] = s1 * fmaf(b[e], 1.f - s1, 1.f);
-          a[e] *= s0;
-          b[e] *= s1;
-        }
-        ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
+        zx[e] = p.silu ? x[e] * sigmoid_f(x[e]) : x[e];
+        zy[e] = p.silu ? y[e] * sigmoid_f(y[e]) : y[e];
+        ss = fmaf(zx[e], zx[e], fmaf(zy[e], zy[e], ss));
       }
       ss = row_sum<D>(ss);
       bool floored;
       const float scale = row_scale<D>(p, ss, floored);
-      const float* w = r.is_k ? p.k_weight : p.q_weight;
       float dot = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        a[e] *= scale;  // the normed row
-        b[e] *= scale;
-        if (w && r.live) {
-          const float ga = da[e] * a[e], gb = db[e] * b[e];
-          dw[0][e] += r.is_k ? 0.f : ga;
-          dw[0][8 + e] += r.is_k ? 0.f : gb;
-          dw[1][e] += r.is_k ? ga : 0.f;
-          dw[1][8 + e] += r.is_k ? gb : 0.f;
-          da[e] *= w[c0 + e];
-          db[e] *= w[c1 + e];
+        zx[e] *= scale;  // the normed row
+        zy[e] *= scale;
+        if (live) {
+          dwa[e] = fmaf(dx[e], zx[e], dwa[e]);
+          dwb[e] = fmaf(dy[e], zy[e], dwb[e]);
         }
-        dot = fmaf(da[e], a[e], fmaf(db[e], b[e], dot));
+        dx[e] *= wa[e];
+        dy[e] *= wb[e];
+        dot = fmaf(dx[e], zx[e], fmaf(dy[e], zy[e], dot));
       }
       dot = row_sum<D>(dot) * (p.l2 ? 1.f : 1.f / D);
       if (floored) dot = 0.f;
-      if (!r.live) continue;
+      if (!live) continue;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        da[e] = scale * (da[e] - a[e] * dot) * sa[e];
-        db[e] = scale * (db[e] - b[e] * dot) * sb[e];
+        dx[e] = scale * (dx[e] - zx[e] * dot);
+        dy[e] = scale * (dy[e] - zy[e] * dot);
+        if (p.silu) {
+          const float g0 = sigmoid_f(x[e]), g1 = sigmoid_f(y[e]);
+          dx[e] *= g0 * fmaf(x[e], 1.f - g0, 1.f);
+          dy[e] *= g1 * fmaf(y[e], 1.f - g1, 1.f);
+        }
       }
-      const long long to = r.is_k ? r.b * p.dks_b + r.t * p.dks_t + r.h * p.dks_h
-                                  : r.b * p.dqs_b + r.t * p.dqs_t + r.h * p.dqs_h;
-      TI* o = static_cast<TI*>(r.is_k ? p.k_out : p.q_out) + to;
-      store_piece(o + c0, da);
-      store_piece(o + c1, db);
+      TI* o = static_cast<TI*>(s.out) + b * s.ob + t * s.ot + at.h * s.oh;
+      store_piece(o + c0, dx);
+      store_piece(o + c1, dy);
     }
   }
   if (!p.partial) return;
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    __syncthreads();
+  for (int e = 0; e < 8; ++e) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      float x = dw[which][e];
-#pragma unroll
-      for (int o = L; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-      if (lane < L) part[warp][(e < 8 ? c0 : c1) + (e & 7)] = x;
+    for (int o = L; o < 32; o <<= 1) {
+      dwa[e] += __shfl_xor_sync(0xffffffffu, dwa[e], o);
+      dwb[e] += __shfl_xor_sync(0xffffffffu, dwb[e], o);
     }
-    __syncthreads();
-    for (int d = threadIdx.x; d < D; d += kThreads) {
-      float x = 0.f;
-#pragma unroll
-      for (int ww = 0; ww < kThreads / 32; ++ww) x += part[ww][d];
-      p.partial[((size_t)blockIdx.x * 2 + which) * D + d] = x;
+    if (lane < L) {
+      part[warp][c0 + e] = dwa[e];
+      part[warp][c1 + e] = dwb[e];
     }
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < D; d += kThreads) {
+    float x = 0.f;
+#pragma unroll
+    for (int ww = 0; ww < kThreads / 32; ++ww) x += part[ww][d];
+    p.partial[((size_t)blockIdx.x * 2 + blockIdx.y) * D + d] = x;
   }
 }
 
@@ -314,15 +329,15 @@ __global__ void __launch_bounds__(256) qk_weight_kernel(const float* partial, in
 
 // Tokens of a tile: about 128 rows, at most kMaxTokens tables of turns.
 int tile_tokens(const QkProblem& p) {
-  const int heads = p.Hq + p.Hk, t = 128 / heads;
+  const int heads = p.Hq > p.Hk ? p.Hq : p.Hk, t = 128 / heads;
   return t < 1 ? 1 : t > kMaxTokens ? kMaxTokens : t;
 }
 
 template <typename TI, int D>
 cudaError_t fwd(const QkProblem& p, cudaStream_t st) {
   const int tokens = tile_tokens(p);
-  const unsigned grid = (unsigned)(((long long)p.B * p.T + tokens - 1) / tokens);
-  const size_t smem = (size_t)tokens * (p.rot / 2) * sizeof(float2);
+  const dim3 grid((unsigned)(((long long)p.B * p.T + tokens - 1) / tokens), 2);
+  const size_t smem = (size_t)tokens * p.rot * sizeof(float);
   if (p.interleaved)
     qk_fwd_kernel<TI, D, true><<<grid, kThreads, smem, st>>>(p, tokens);
   else
@@ -333,15 +348,15 @@ cudaError_t fwd(const QkProblem& p, cudaStream_t st) {
 template <typename TI, typename TG, int D>
 cudaError_t bwd(const QkProblem& p, cudaStream_t st) {
   const int tokens = tile_tokens(p);
-  const unsigned grid = (unsigned)qk_bwd_ctas(p.B, p.T, p.Hq, p.Hk);
-  const size_t smem = (size_t)tokens * (p.rot / 2) * sizeof(float2);
+  const unsigned ctas = (unsigned)qk_bwd_ctas(p.B, p.T, p.Hq, p.Hk);
+  const size_t smem = (size_t)tokens * p.rot * sizeof(float);
   if (p.interleaved)
-    qk_bwd_kernel<TI, TG, D, true><<<grid, kThreads, smem, st>>>(p, tokens);
+    qk_bwd_kernel<TI, TG, D, true><<<dim3(ctas, 2), kThreads, smem, st>>>(p, tokens);
   else
-    qk_bwd_kernel<TI, TG, D, false><<<grid, kThreads, smem, st>>>(p, tokens);
+    qk_bwd_kernel<TI, TG, D, false><<<dim3(ctas, 2), kThreads, smem, st>>>(p, tokens);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.partial) return e;
-  qk_weight_kernel<<<2 * D / 8, 256, 0, st>>>(p.partial, (int)grid, D, p.dq_weight, p.dk_weight);
+  qk_weight_kernel<<<2 * D / 8, 256, 0, st>>>(p.partial, (int)ctas, D, p.dq_weight, p.dk_weight);
   return cudaGetLastError();
 }
 
@@ -358,7 +373,7 @@ int qk_bwd_ctas(int B, int T, int Hq, int Hk) {
   p.Hk = Hk;
   const int tokens = tile_tokens(p);
   const long long tiles = ((long long)B * T + tokens - 1) / tokens;
-  constexpr long long kCtas = 148 * 3;  // what the register use leaves resident on 148 SMs
+  constexpr long long kCtas = 148 * 2;  // times two tensors: what is resident on 148 SMs
   return (int)(tiles < kCtas ? tiles : kCtas);
 }
 
