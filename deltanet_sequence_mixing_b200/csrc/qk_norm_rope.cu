@@ -24,6 +24,8 @@
 // computes them once for a token and uses them for all of its heads.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -32,22 +34,50 @@ namespace {
 
 constexpr int kThreads = 256, kMaxTokens = 16;
 
-template <int N>
-__device__ __forceinline__ void load_piece(const float* p, float (&x)[N]) {
+// Eight values of a row as four pairs, in two-wide arithmetic: a row's work is
+// mostly instructions beside its loads (one value at a time the forward of B4
+// T4096 H16 D128 took 64.5 us, the gradient 139 us).
+struct V8 {
+  float2 v[4];
+};
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{ .reg .b64 x, y, z, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7};"
+      " fma.rn.f32x2 w, x, y, z; mov.b64 {%0, %1}, w; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+__device__ __forceinline__ void load_piece(const float* p, V8& x) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  x.v[0] = make_float2(a.x, a.y);
+  x.v[1] = make_float2(a.z, a.w);
+  x.v[2] = make_float2(b.x, b.y);
+  x.v[3] = make_float2(b.z, b.w);
+}
+__device__ __forceinline__ void load_piece(const __nv_bfloat16* p, V8& x) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < N; i += 4) {
-    const float4 v = *reinterpret_cast<const float4*>(p + i);
-    x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
-  }
+  for (int i = 0; i < 4; ++i) x.v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
-__device__ __forceinline__ void load_piece(const __nv_bfloat16* p, float (&x)[8]) {
-  unpack_bf16x8(*reinterpret_cast<const uint4*>(p), x);
+__device__ __forceinline__ void store_piece(float* p, const V8& x) {
+  *reinterpret_cast<float4*>(p) = make_float4(x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y);
 }
-__device__ __forceinline__ void store_piece(float* p, const float (&x)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+__device__ __forceinline__ void store_piece(__nv_bfloat16* p, const V8& x) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack2_bf16(x.v[0].x, x.v[0].y), pack2_bf16(x.v[1].x, x.v[1].y),
+                                            pack2_bf16(x.v[2].x, x.v[2].y), pack2_bf16(x.v[3].x, x.v[3].y));
 }
-__device__ __forceinline__ void store_piece(__nv_bfloat16* p, const float (&x)[8]) { st_bf16x8(p, x); }
 
 // Column of a lane's two pieces: pairs of pieces of the rotated halves first,
 // then neighbours.
@@ -62,29 +92,46 @@ __device__ __forceinline__ void pieces_of(int l, int rot, int interleaved, int& 
   }
 }
 
-// The turn by +angle (way = 1) or -angle (way = -1) of a lane's 16 values: the
-// cosines and sines of its 8 pairs stand in a row.
-template <bool INTER>
-__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float* cs, const float* sn, float way) {
-  float c[8], s[8];
+// The turn by +angle, or back by it, of a lane's 16 values: the cosines and
+// sines of its 8 pairs stand in a row.
+template <bool INTER, bool BACK>
+__device__ __forceinline__ void turn(V8& a, V8& b, const float* cs, const float* sn) {
+  V8 c, s;
   load_piece(cs, c);
   load_piece(sn, s);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float& x = INTER ? (i < 4 ? a[2 * (i & 3)] : b[2 * (i & 3)]) : a[i];
-    float& y = INTER ? (i < 4 ? a[2 * (i & 3) + 1] : b[2 * (i & 3) + 1]) : b[i];
-    const float x0 = x, ws = way * s[i];
-    x = x0 * c[i] - y * ws;
-    y = y * c[i] + x0 * ws;
+  for (int i = 0; i < 4; ++i) {
+    if (INTER) {  // pairs 2 i and 2 i + 1: in a (i < 2) or b
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float2& x = (i < 2 ? a : b).v[(2 * i + h) & 3];
+        const float cc = h ? c.v[i].y : c.v[i].x, sh = h ? s.v[i].y : s.v[i].x, ss = BACK ? -sh : sh;
+        x = make_float2(x.x * cc - x.y * ss, x.y * cc + x.x * ss);
+      }
+    } else {
+      const float2 n = make_float2(-s.v[i].x, -s.v[i].y), x = a.v[i], y = b.v[i];
+      a.v[i] = fma2(y, BACK ? s.v[i] : n, mul2(x, c.v[i]));
+      b.v[i] = fma2(x, BACK ? n : s.v[i], mul2(y, c.v[i]));
+    }
   }
 }
 
 __device__ __forceinline__ float sigmoid_f(float x) { return 1.f / (1.f + __expf(-x)); }
+__device__ __forceinline__ float2 silu2(float2 x) { return make_float2(x.x * sigmoid_f(x.x), x.y * sigmoid_f(x.y)); }
 
-// cos and sin of the angles of tokens [n0, n0 + nt) (flat over B x T): `half`
-// cosines, then as many sines, for each token.
-__device__ __forceinline__ void fill_turns(const QkProblem& p, int n0, int nt, float* turns) {
+// What a tile's rows share, for each of its tokens: where its row of the input
+// and of the output begins (head 0), and `half` cosines, then as many sines.
+struct Tile {
+  long long in[kMaxTokens], out[kMaxTokens];
+};
+__device__ __forceinline__ void fill_tile(const QkProblem& p, int n0, int nt, long long xb, long long xt, long long hb,
+                                          long long ht, Tile& tile, float* turns) {
   const int half = p.rot / 2;
+  if (threadIdx.x < nt) {
+    const int b = (n0 + (int)threadIdx.x) / p.T, t = n0 + (int)threadIdx.x - b * p.T;
+    tile.in[threadIdx.x] = b * xb + t * xt;
+    tile.out[threadIdx.x] = b * hb + t * ht;
+  }
   for (int i = threadIdx.x; i < nt * half; i += kThreads) {
     const int tok = i / half, f = i - tok * half, b = (n0 + tok) / p.T, t = (n0 + tok) - b * p.T;
     const double pos = p.positions ? (double)p.positions[b * p.pos_stride_b + t] : (double)t;
@@ -98,27 +145,28 @@ __device__ __forceinline__ void fill_turns(const QkProblem& p, int n0, int nt, f
 }
 
 template <int D>
-__device__ __forceinline__ float row_sum(float x) {  // over the D / 16 lanes of a row
+__device__ __forceinline__ float row_sum(float2 x) {  // over the D / 16 lanes of a row
+  float y = x.x + x.y;
 #pragma unroll
-  for (int o = D / 32; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
+  for (int o = D / 32; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+  return y;
 }
 
-template <int D>
-__device__ __forceinline__ float row_scale(const QkProblem& p, float ss, bool& floored) {
-  if (p.l2) {
-    const float norm = sqrtf(ss);
-    floored = norm < p.eps;  // false for a NaN, which stays one
-    return 1.f / (floored ? p.eps : norm);
-  }
+template <int D, bool L2>
+__device__ __forceinline__ float row_scale(float eps, float ss, bool& floored) {
   floored = false;
-  return rsqrtf(ss * (1.f / D) + p.eps);
+  if (L2) {
+    const float norm = sqrtf(ss);
+    floored = norm < eps;  // false for a NaN, which stays one
+    return 1.f / (floored ? eps : norm);
+  }
+  return rsqrtf(ss * (1.f / D) + eps);
 }
 
 // One tensor of the two, as a CTA sees it.
 struct Side {
   const void* x;
-  const void* g;       // gradient: the derivative by the output
+  const void* g;  // gradient: the derivative by the output
   const float* w;
   void* out;
   int H;
@@ -151,10 +199,11 @@ struct Walk {
   }
 };
 
-template <typename TI, int D, bool INTER>
+template <typename TI, int D, bool INTER, bool L2, bool SILU>
 __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkProblem p, int tokens) {
   constexpr int L = D / 16, ROWS = kThreads / L;
   extern __shared__ float turns[];
+  __shared__ Tile tile;
   const Side s = side_of(p, blockIdx.y);
   const int N = p.B * p.T, n0 = (int)blockIdx.x * tokens, nt = min(tokens, N - n0), half = p.rot / 2;
   const int l = threadIdx.x % L;
@@ -162,44 +211,45 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkProblem p, int
   int c0, c1;
   pieces_of(l, p.rot, INTER, c0, c1);
   const bool turned = l < p.rot / 16;
-  float wa[8], wb[8];
+  V8 wa, wb;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    wa[e] = s.w ? s.w[c0 + e] : 1.f;
-    wb[e] = s.w ? s.w[c1 + e] : 1.f;
+  for (int e = 0; e < 4; ++e) {
+    wa.v[e] = s.w ? make_float2(s.w[c0 + 2 * e], s.w[c0 + 2 * e + 1]) : both(1.f);
+    wb.v[e] = s.w ? make_float2(s.w[c1 + 2 * e], s.w[c1 + 2 * e + 1]) : both(1.f);
   }
-  if (half) fill_turns(p, n0, nt, turns);
+  const long long oh = (long long)p.T * D;
+  fill_tile(p, n0, nt, s.xb, s.xt, oh * s.H, D, tile, turns);
   __syncthreads();
   Walk<ROWS> at(threadIdx.x / L, s.H);
   for (int i0 = 0; i0 < nt * s.H; i0 += ROWS, at.step()) {
     const bool live = at.tok < nt;
-    const int n = n0 + at.tok, b = n / p.T, t = n - b * p.T;
-    float x[8] = {}, y[8] = {};
+    V8 x = {}, y = {};
     if (live) {
-      const TI* in = static_cast<const TI*>(s.x) + b * s.xb + t * s.xt + at.h * s.xh;
+      const TI* in = static_cast<const TI*>(s.x) + tile.in[at.tok] + at.h * s.xh;
       load_piece(in + c0, x);
       load_piece(in + c1, y);
     }
-    float ss = 0.f;
+    float2 ss = both(0.f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (p.silu) {
-        x[e] *= sigmoid_f(x[e]);
-        y[e] *= sigmoid_f(y[e]);
+    for (int e = 0; e < 4; ++e) {
+      if (SILU) {
+        x.v[e] = silu2(x.v[e]);
+        y.v[e] = silu2(y.v[e]);
       }
-      ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
+      ss = fma2(x.v[e], x.v[e], fma2(y.v[e], y.v[e], ss));
     }
-    ss = row_sum<D>(ss);
+    const float sum = row_sum<D>(ss);
     if (!live) continue;
     bool floored;
-    const float scale = row_scale<D>(p, ss, floored);
+    const float2 scale = both(row_scale<D, L2>(p.eps, sum, floored));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[e] *= scale * wa[e];
-      y[e] *= scale * wb[e];
+    for (int e = 0; e < 4; ++e) {
+      x.v[e] = mul2(x.v[e], mul2(scale, wa.v[e]));
+      y.v[e] = mul2(y.v[e], mul2(scale, wb.v[e]));
     }
-    if (turned) turn<INTER>(x, y, turns + 2 * half * at.tok + 8 * l, turns + 2 * half * at.tok + half + 8 * l, 1.f);
-    TI* o = static_cast<TI*>(s.out) + (((long long)b * s.H + at.h) * p.T + t) * D;
+    const float* cs = turns + 2 * half * at.tok + 8 * l;
+    if (turned) turn<INTER, false>(x, y, cs, cs + half);
+    TI* o = static_cast<TI*>(s.out) + tile.out[at.tok] + at.h * oh;
     store_piece(o + c0, x);
     store_piece(o + c1, y);
   }
@@ -208,10 +258,12 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkProblem p, int
 // Gradient.  CTAs walk the token tiles with a stride, so that the weights'
 // gradients stay in registers until the end; every CTA then leaves its row of
 // partial sums and a second kernel adds them in a fixed order.
-template <typename TI, typename TG, int D, bool INTER>
+template <typename TI, typename TG, int D, bool INTER, bool L2, bool SILU>
 __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkProblem p, int tokens) {
   constexpr int L = D / 16, ROWS = kThreads / L;
   extern __shared__ float turns[];
+  __shared__ Tile tile;  // in: of x; out: of the derivative by the output
+  __shared__ long long place[kMaxTokens];
   __shared__ float part[kThreads / 32][D];
   const Side s = side_of(p, blockIdx.y);
   const int N = p.B * p.T, half = p.rot / 2;
@@ -219,70 +271,77 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkProblem p, int
   int c0, c1;
   pieces_of(l, p.rot, INTER, c0, c1);
   const bool turned = l < p.rot / 16;
-  float wa[8], wb[8], dwa[8] = {}, dwb[8] = {};
+  V8 wa, wb, dwa = {}, dwb = {};
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    wa[e] = s.w ? s.w[c0 + e] : 1.f;
-    wb[e] = s.w ? s.w[c1 + e] : 1.f;
+  for (int e = 0; e < 4; ++e) {
+    wa.v[e] = s.w ? make_float2(s.w[c0 + 2 * e], s.w[c0 + 2 * e + 1]) : both(1.f);
+    wb.v[e] = s.w ? make_float2(s.w[c1 + 2 * e], s.w[c1 + 2 * e + 1]) : both(1.f);
   }
+  const long long gh = (long long)p.T * D;
   for (long long first = (long long)blockIdx.x * tokens; s.H > 0 && first < N; first += (long long)gridDim.x * tokens) {
     const int n0 = (int)first, nt = min(tokens, N - n0);
-    __syncthreads();  // the turns of the tile before have been read
-    if (half) fill_turns(p, n0, nt, turns);
+    __syncthreads();  // the tile before has been worked on
+    fill_tile(p, n0, nt, s.xb, s.xt, gh * s.H, D, tile, turns);
+    if (threadIdx.x < nt) {
+      const int b = (n0 + (int)threadIdx.x) / p.T, t = n0 + (int)threadIdx.x - b * p.T;
+      place[threadIdx.x] = b * s.ob + t * s.ot;
+    }
     __syncthreads();
     Walk<ROWS> at(threadIdx.x / L, s.H);
     for (int i0 = 0; i0 < nt * s.H; i0 += ROWS, at.step()) {
       const bool live = at.tok < nt;
-      const int n = n0 + at.tok, b = n / p.T, t = n - b * p.T;
-      float x[8] = {}, y[8] = {}, dx[8] = {}, dy[8] = {};
+      V8 x = {}, y = {}, dx = {}, dy = {};
       if (live) {
-        const TI* in = static_cast<const TI*>(s.x) + b * s.xb + t * s.xt + at.h * s.xh;
-        const TG* g = static_cast<const TG*>(s.g) + (((long long)b * s.H + at.h) * p.T + t) * D;
+        const TI* in = static_cast<const TI*>(s.x) + tile.in[at.tok] + at.h * s.xh;
+        const TG* g = static_cast<const TG*>(s.g) + tile.out[at.tok] + at.h * gh;
         load_piece(in + c0, x);
         load_piece(in + c1, y);
         load_piece(g + c0, dx);
         load_piece(g + c1, dy);
-        if (turned)
-          turn<INTER>(dx, dy, turns + 2 * half * at.tok + 8 * l, turns + 2 * half * at.tok + half + 8 * l, -1.f);
       }
-      // z over x in place; silu' is formed again from x at the end
-      float ss = 0.f, zx[8], zy[8];
+      V8 zx, zy;
+      float2 ss = both(0.f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        zx[e] = p.silu ? x[e] * sigmoid_f(x[e]) : x[e];
-        zy[e] = p.silu ? y[e] * sigmoid_f(y[e]) : y[e];
-        ss = fmaf(zx[e], zx[e], fmaf(zy[e], zy[e], ss));
+      for (int e = 0; e < 4; ++e) {
+        zx.v[e] = SILU ? silu2(x.v[e]) : x.v[e];
+        zy.v[e] = SILU ? silu2(y.v[e]) : y.v[e];
+        ss = fma2(zx.v[e], zx.v[e], fma2(zy.v[e], zy.v[e], ss));
       }
-      ss = row_sum<D>(ss);
+      const float* cs = turns + 2 * half * at.tok + 8 * l;
+      if (live && turned) turn<INTER, true>(dx, dy, cs, cs + half);
       bool floored;
-      const float scale = row_scale<D>(p, ss, floored);
-      float dot = 0.f;
+      const float2 scale = both(row_scale<D, L2>(p.eps, row_sum<D>(ss), floored));
+      float2 dots = both(0.f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        zx[e] *= scale;  // the normed row
-        zy[e] *= scale;
+      for (int e = 0; e < 4; ++e) {
+        zx.v[e] = mul2(zx.v[e], scale);  // the normed row
+        zy.v[e] = mul2(zy.v[e], scale);
         if (live) {
-          dwa[e] = fmaf(dx[e], zx[e], dwa[e]);
-          dwb[e] = fmaf(dy[e], zy[e], dwb[e]);
+          dwa.v[e] = fma2(dx.v[e], zx.v[e], dwa.v[e]);
+          dwb.v[e] = fma2(dy.v[e], zy.v[e], dwb.v[e]);
         }
-        dx[e] *= wa[e];
-        dy[e] *= wb[e];
-        dot = fmaf(dx[e], zx[e], fmaf(dy[e], zy[e], dot));
+        dx.v[e] = mul2(dx.v[e], wa.v[e]);
+        dy.v[e] = mul2(dy.v[e], wb.v[e]);
+        dots = fma2(dx.v[e], zx.v[e], fma2(dy.v[e], zy.v[e], dots));
       }
-      dot = row_sum<D>(dot) * (p.l2 ? 1.f : 1.f / D);
+      float dot = row_sum<D>(dots) * (L2 ? 1.f : 1.f / D);
       if (floored) dot = 0.f;
       if (!live) continue;
+      const float2 less = both(-dot);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        dx[e] = scale * (dx[e] - zx[e] * dot);
-        dy[e] = scale * (dy[e] - zy[e] * dot);
-        if (p.silu) {
-          const float g0 = sigmoid_f(x[e]), g1 = sigmoid_f(y[e]);
-          dx[e] *= g0 * fmaf(x[e], 1.f - g0, 1.f);
-          dy[e] *= g1 * fmaf(y[e], 1.f - g1, 1.f);
+      for (int e = 0; e < 4; ++e) {
+        dx.v[e] = mul2(scale, fma2(zx.v[e], less, dx.v[e]));
+        dy.v[e] = mul2(scale, fma2(zy.v[e], less, dy.v[e]));
+        if (SILU) {
+          auto slope = [](float v) {
+            const float g = sigmoid_f(v);
+            return g * fmaf(v, 1.f - g, 1.f);
+          };
+          dx.v[e] = mul2(dx.v[e], make_float2(slope(x.v[e].x), slope(x.v[e].y)));
+          dy.v[e] = mul2(dy.v[e], make_float2(slope(y.v[e].x), slope(y.v[e].y)));
         }
       }
-      TI* o = static_cast<TI*>(s.out) + b * s.ob + t * s.ot + at.h * s.oh;
+      TI* o = static_cast<TI*>(s.out) + place[at.tok] + at.h * s.oh;
       store_piece(o + c0, dx);
       store_piece(o + c1, dy);
     }
@@ -290,14 +349,15 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkProblem p, int
   if (!p.partial) return;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
+    float a = e & 1 ? dwa.v[e / 2].y : dwa.v[e / 2].x, b = e & 1 ? dwb.v[e / 2].y : dwb.v[e / 2].x;
 #pragma unroll
     for (int o = L; o < 32; o <<= 1) {
-      dwa[e] += __shfl_xor_sync(0xffffffffu, dwa[e], o);
-      dwb[e] += __shfl_xor_sync(0xffffffffu, dwb[e], o);
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      b += __shfl_xor_sync(0xffffffffu, b, o);
     }
     if (lane < L) {
-      part[warp][c0 + e] = dwa[e];
-      part[warp][c1 + e] = dwb[e];
+      part[warp][c0 + e] = a;
+      part[warp][c1 + e] = b;
     }
   }
   __syncthreads();
@@ -327,10 +387,31 @@ __global__ void __launch_bounds__(256) qk_weight_kernel(const float* partial, in
   }
 }
 
-// Tokens of a tile: about 128 rows, at most kMaxTokens tables of turns.
+// Tokens of a tile: about 256 rows, at most kMaxTokens tables of turns.
 int tile_tokens(const QkProblem& p) {
-  const int heads = p.Hq > p.Hk ? p.Hq : p.Hk, t = 128 / heads;
+  const int heads = p.Hq > p.Hk ? p.Hq : p.Hk, t = 256 / heads;
   return t < 1 ? 1 : t > kMaxTokens ? kMaxTokens : t;
+}
+
+// f(INTER, L2, SILU) for the problem's options.
+template <typename F>
+void by_options(const QkProblem& p, F f) {
+  auto silu = [&](auto inter, auto l2) {
+    if (p.silu)
+      f(inter, l2, std::true_type{});
+    else
+      f(inter, l2, std::false_type{});
+  };
+  auto norm = [&](auto inter) {
+    if (p.l2)
+      silu(inter, std::true_type{});
+    else
+      silu(inter, std::false_type{});
+  };
+  if (p.interleaved)
+    norm(std::true_type{});
+  else
+    norm(std::false_type{});
 }
 
 template <typename TI, int D>
@@ -338,10 +419,9 @@ cudaError_t fwd(const QkProblem& p, cudaStream_t st) {
   const int tokens = tile_tokens(p);
   const dim3 grid((unsigned)(((long long)p.B * p.T + tokens - 1) / tokens), 2);
   const size_t smem = (size_t)tokens * p.rot * sizeof(float);
-  if (p.interleaved)
-    qk_fwd_kernel<TI, D, true><<<grid, kThreads, smem, st>>>(p, tokens);
-  else
-    qk_fwd_kernel<TI, D, false><<<grid, kThreads, smem, st>>>(p, tokens);
+  by_options(p, [&](auto inter, auto l2, auto silu) {
+    qk_fwd_kernel<TI, D, inter(), l2(), silu()><<<grid, kThreads, smem, st>>>(p, tokens);
+  });
   return cudaGetLastError();
 }
 
@@ -350,10 +430,9 @@ cudaError_t bwd(const QkProblem& p, cudaStream_t st) {
   const int tokens = tile_tokens(p);
   const unsigned ctas = (unsigned)qk_bwd_ctas(p.B, p.T, p.Hq, p.Hk);
   const size_t smem = (size_t)tokens * p.rot * sizeof(float);
-  if (p.interleaved)
-    qk_bwd_kernel<TI, TG, D, true><<<dim3(ctas, 2), kThreads, smem, st>>>(p, tokens);
-  else
-    qk_bwd_kernel<TI, TG, D, false><<<dim3(ctas, 2), kThreads, smem, st>>>(p, tokens);
+  by_options(p, [&](auto inter, auto l2, auto silu) {
+    qk_bwd_kernel<TI, TG, D, inter(), l2(), silu()><<<dim3(ctas, 2), kThreads, smem, st>>>(p, tokens);
+  });
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.partial) return e;
   qk_weight_kernel<<<2 * D / 8, 256, 0, st>>>(p.partial, (int)ctas, D, p.dq_weight, p.dk_weight);
