@@ -220,8 +220,8 @@ struct QkProblem {
   float eps;
   int l2, silu, interleaved, bf16, grad_bf16;
 };
-// CTAs (rows of partial weight sums) of the gradient.
-int qk_bwd_ctas(int B, int T, int Hq, int Hk);
+// CTAs (rows of partial weight sums) of the gradient: most without the silu.
+int qk_bwd_ctas(int B, int T, int Hq, int Hk, int silu);
 cudaError_t launch_qk_fwd(const QkProblem& p, cudaStream_t st);
 cudaError_t launch_qk_bwd(const QkProblem& p, cudaStream_t st);
 

@@ -119,19 +119,23 @@ __device__ __forceinline__ void turn(V8& a, V8& b, const float* cs, const float*
 __device__ __forceinline__ float sigmoid_f(float x) { return 1.f / (1.f + __expf(-x)); }
 __device__ __forceinline__ float2 silu2(float2 x) { return make_float2(x.x * sigmoid_f(x.x), x.y * sigmoid_f(x.y)); }
 
-// What a tile's rows share, for each of its tokens: where its row of the input
-// and of the output begins (head 0), and `half` cosines, then as many sines.
+// Where the rows of a tile's tokens begin (head 0) in the input and the output.
 struct Tile {
   long long in[kMaxTokens], out[kMaxTokens];
 };
-__device__ __forceinline__ void fill_tile(const QkProblem& p, int n0, int nt, long long xb, long long xt, long long hb,
-                                          long long ht, Tile& tile, float* turns) {
-  const int half = p.rot / 2;
+__device__ __forceinline__ void fill_tile(const QkProblem& p, int n0, int nt, long long xb, long long xt, long long ob,
+                                          long long ot, Tile& tile) {
   if (threadIdx.x < nt) {
     const int b = (n0 + (int)threadIdx.x) / p.T, t = n0 + (int)threadIdx.x - b * p.T;
     tile.in[threadIdx.x] = b * xb + t * xt;
-    tile.out[threadIdx.x] = b * hb + t * ht;
+    tile.out[threadIdx.x] = b * ob + t * ot;
   }
+}
+
+// cos and sin of the angles of tokens [n0, n0 + nt) (flat over B x T): `half`
+// cosines, then as many sines, for each token.
+__device__ __forceinline__ void fill_turns(const QkProblem& p, int n0, int nt, float* turns) {
+  const int half = p.rot / 2;
   for (int i = threadIdx.x; i < nt * half; i += kThreads) {
     const int tok = i / half, f = i - tok * half, b = (n0 + tok) / p.T, t = (n0 + tok) - b * p.T;
     const double pos = p.positions ? (double)p.positions[b * p.pos_stride_b + t] : (double)t;
@@ -203,55 +207,64 @@ template <typename TI, int D, bool INTER, bool L2, bool SILU>
 __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkProblem p, int tokens) {
   constexpr int L = D / 16, ROWS = kThreads / L;
   extern __shared__ float turns[];
-  __shared__ Tile tile;
-  const Side s = side_of(p, blockIdx.y);
+  __shared__ Tile tile[2];
   const int N = p.B * p.T, n0 = (int)blockIdx.x * tokens, nt = min(tokens, N - n0), half = p.rot / 2;
   const int l = threadIdx.x % L;
-  if (s.H == 0) return;
   int c0, c1;
   pieces_of(l, p.rot, INTER, c0, c1);
   const bool turned = l < p.rot / 16;
-  V8 wa, wb;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    wa.v[e] = s.w ? make_float2(s.w[c0 + 2 * e], s.w[c0 + 2 * e + 1]) : both(1.f);
-    wb.v[e] = s.w ? make_float2(s.w[c1 + 2 * e], s.w[c1 + 2 * e + 1]) : both(1.f);
-  }
   const long long oh = (long long)p.T * D;
-  fill_tile(p, n0, nt, s.xb, s.xt, oh * s.H, D, tile, turns);
+  fill_turns(p, n0, nt, turns);
+  // both tensors, or by blockIdx.y one of them
+  const int first = gridDim.y == 1 ? 0 : blockIdx.y, last = gridDim.y == 1 ? 1 : blockIdx.y;
+  for (int key = first; key <= last; ++key) {
+    const Side s = side_of(p, key);
+    fill_tile(p, n0, nt, s.xb, s.xt, oh * s.H, D, tile[key]);
+  }
   __syncthreads();
-  Walk<ROWS> at(threadIdx.x / L, s.H);
-  for (int i0 = 0; i0 < nt * s.H; i0 += ROWS, at.step()) {
-    const bool live = at.tok < nt;
-    V8 x = {}, y = {};
-    if (live) {
-      const TI* in = static_cast<const TI*>(s.x) + tile.in[at.tok] + at.h * s.xh;
-      load_piece(in + c0, x);
-      load_piece(in + c1, y);
-    }
-    float2 ss = both(0.f);
+#pragma unroll 1
+  for (int key = first; key <= last; ++key) {
+    const Side s = side_of(p, key);
+    if (s.H == 0) continue;
+    V8 wa, wb;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      if (SILU) {
-        x.v[e] = silu2(x.v[e]);
-        y.v[e] = silu2(y.v[e]);
+      wa.v[e] = s.w ? make_float2(s.w[c0 + 2 * e], s.w[c0 + 2 * e + 1]) : both(1.f);
+      wb.v[e] = s.w ? make_float2(s.w[c1 + 2 * e], s.w[c1 + 2 * e + 1]) : both(1.f);
+    }
+    Walk<ROWS> at(threadIdx.x / L, s.H);
+    for (int i0 = 0; i0 < nt * s.H; i0 += ROWS, at.step()) {
+      const bool live = at.tok < nt;
+      V8 x = {}, y = {};
+      if (live) {
+        const TI* in = static_cast<const TI*>(s.x) + tile[key].in[at.tok] + at.h * s.xh;
+        load_piece(in + c0, x);
+        load_piece(in + c1, y);
       }
-      ss = fma2(x.v[e], x.v[e], fma2(y.v[e], y.v[e], ss));
-    }
-    const float sum = row_sum<D>(ss);
-    if (!live) continue;
-    bool floored;
-    const float2 scale = both(row_scale<D, L2>(p.eps, sum, floored));
+      float2 ss = both(0.f);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x.v[e] = mul2(x.v[e], mul2(scale, wa.v[e]));
-      y.v[e] = mul2(y.v[e], mul2(scale, wb.v[e]));
+      for (int e = 0; e < 4; ++e) {
+        if (SILU) {
+          x.v[e] = silu2(x.v[e]);
+          y.v[e] = silu2(y.v[e]);
+        }
+        ss = fma2(x.v[e], x.v[e], fma2(y.v[e], y.v[e], ss));
+      }
+      const float sum = row_sum<D>(ss);
+      if (!live) continue;
+      bool floored;
+      const float2 scale = both(row_scale<D, L2>(p.eps, sum, floored));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x.v[e] = mul2(x.v[e], mul2(scale, wa.v[e]));
+        y.v[e] = mul2(y.v[e], mul2(scale, wb.v[e]));
+      }
+      const float* cs = turns + 2 * half * at.tok + 8 * l;
+      if (turned) turn<INTER, false>(x, y, cs, cs + half);
+      TI* o = static_cast<TI*>(s.out) + tile[key].out[at.tok] + at.h * oh;
+      store_piece(o + c0, x);
+      store_piece(o + c1, y);
     }
-    const float* cs = turns + 2 * half * at.tok + 8 * l;
-    if (turned) turn<INTER, false>(x, y, cs, cs + half);
-    TI* o = static_cast<TI*>(s.out) + tile.out[at.tok] + at.h * oh;
-    store_piece(o + c0, x);
-    store_piece(o + c1, y);
   }
 }
 
@@ -259,11 +272,10 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkProblem p, int
 // gradients stay in registers until the end; every CTA then leaves its row of
 // partial sums and a second kernel adds them in a fixed order.
 template <typename TI, typename TG, int D, bool INTER, bool L2, bool SILU>
-__global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkProblem p, int tokens) {
+__global__ void __launch_bounds__(kThreads, SILU ? 2 : 3) qk_bwd_kernel(const QkProblem p, int tokens) {
   constexpr int L = D / 16, ROWS = kThreads / L;
   extern __shared__ float turns[];
-  __shared__ Tile tile;  // in: of x; out: of the derivative by the output
-  __shared__ long long place[kMaxTokens];
+  __shared__ Tile tile, place;  // of x and of the derivative by the output; of the derivative by x
   __shared__ float part[kThreads / 32][D];
   const Side s = side_of(p, blockIdx.y);
   const int N = p.B * p.T, half = p.rot / 2;
@@ -281,11 +293,9 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkProblem p, int
   for (long long first = (long long)blockIdx.x * tokens; s.H > 0 && first < N; first += (long long)gridDim.x * tokens) {
     const int n0 = (int)first, nt = min(tokens, N - n0);
     __syncthreads();  // the tile before has been worked on
-    fill_tile(p, n0, nt, s.xb, s.xt, gh * s.H, D, tile, turns);
-    if (threadIdx.x < nt) {
-      const int b = (n0 + (int)threadIdx.x) / p.T, t = n0 + (int)threadIdx.x - b * p.T;
-      place[threadIdx.x] = b * s.ob + t * s.ot;
-    }
+    fill_turns(p, n0, nt, turns);
+    fill_tile(p, n0, nt, s.xb, s.xt, gh * s.H, D, tile);
+    fill_tile(p, n0, nt, s.ob, s.ot, 0, 0, place);
     __syncthreads();
     Walk<ROWS> at(threadIdx.x / L, s.H);
     for (int i0 = 0; i0 < nt * s.H; i0 += ROWS, at.step()) {
@@ -341,7 +351,7 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkProblem p, int
           dy.v[e] = mul2(dy.v[e], make_float2(slope(y.v[e].x), slope(y.v[e].y)));
         }
       }
-      TI* o = static_cast<TI*>(s.out) + place[at.tok] + at.h * s.oh;
+      TI* o = static_cast<TI*>(s.out) + place.in[at.tok] + at.h * s.oh;
       store_piece(o + c0, dx);
       store_piece(o + c1, dy);
     }
@@ -393,6 +403,11 @@ int tile_tokens(const QkProblem& p) {
   return t < 1 ? 1 : t > kMaxTokens ? kMaxTokens : t;
 }
 
+// With tiles enough for four CTAs on every SM, one CTA takes queries and keys, so
+// that a token's sines are formed once (62.8 us a pass each in a CTA of its own
+// at B4 T4096 H16 D128); with fewer the two run side by side.
+constexpr unsigned kManyTiles = 148 * 4;
+
 // f(INTER, L2, SILU) for the problem's options.
 template <typename F>
 void by_options(const QkProblem& p, F f) {
@@ -417,7 +432,8 @@ void by_options(const QkProblem& p, F f) {
 template <typename TI, int D>
 cudaError_t fwd(const QkProblem& p, cudaStream_t st) {
   const int tokens = tile_tokens(p);
-  const dim3 grid((unsigned)(((long long)p.B * p.T + tokens - 1) / tokens), 2);
+  const unsigned tiles = (unsigned)(((long long)p.B * p.T + tokens - 1) / tokens);
+  const dim3 grid(tiles, tiles >= kManyTiles ? 1 : 2);
   const size_t smem = (size_t)tokens * p.rot * sizeof(float);
   by_options(p, [&](auto inter, auto l2, auto silu) {
     qk_fwd_kernel<TI, D, inter(), l2(), silu()><<<grid, kThreads, smem, st>>>(p, tokens);
@@ -428,7 +444,7 @@ cudaError_t fwd(const QkProblem& p, cudaStream_t st) {
 template <typename TI, typename TG, int D>
 cudaError_t bwd(const QkProblem& p, cudaStream_t st) {
   const int tokens = tile_tokens(p);
-  const unsigned ctas = (unsigned)qk_bwd_ctas(p.B, p.T, p.Hq, p.Hk);
+  const unsigned ctas = (unsigned)qk_bwd_ctas(p.B, p.T, p.Hq, p.Hk, p.silu);
   const size_t smem = (size_t)tokens * p.rot * sizeof(float);
   by_options(p, [&](auto inter, auto l2, auto silu) {
     qk_bwd_kernel<TI, TG, D, inter(), l2(), silu()><<<dim3(ctas, 2), kThreads, smem, st>>>(p, tokens);
@@ -446,14 +462,17 @@ cudaError_t bwd_d(const QkProblem& p, cudaStream_t st) {
 
 }  // namespace
 
-int qk_bwd_ctas(int B, int T, int Hq, int Hk) {
+int qk_bwd_ctas(int B, int T, int Hq, int Hk, int silu) {
   QkProblem p{};
   p.Hq = Hq;
   p.Hk = Hk;
   const int tokens = tile_tokens(p);
   const long long tiles = ((long long)B * T + tokens - 1) / tokens;
-  constexpr long long kCtas = 148 * 2;  // times two tensors: what is resident on 148 SMs
-  return (int)(tiles < kCtas ? tiles : kCtas);
+  // times two tensors: one wave of what is resident on 148 SMs (92 us at B4 T4096
+  // H16 D128; a third more CTAs, and so a second wave, 113 us).  The silu's
+  // derivative takes registers for two CTAs an SM instead of three.
+  const long long ctas = silu ? 148 : 148 * 3 / 2;
+  return (int)(tiles < ctas ? tiles : ctas);
 }
 
 cudaError_t launch_qk_fwd(const QkProblem& p, cudaStream_t st) {
