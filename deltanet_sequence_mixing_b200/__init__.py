@@ -289,32 +289,13 @@ def deltanet_decode_step(q, k, v, beta, S, alpha=None, o=None, prestep: bool = F
 
 # The calls below serve single tokens too, where the host's time is the call's:
 # checks take one short path when nothing is wrong, addresses go to ctypes as
-# integers, and the device is switched only when it is another.
+# integers, and a call for another device than the current one starts over there.
+_current_device = torch._C._cuda_getDevice
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _at(t):
     return None if t is None else t.data_ptr()
-
-
-def _raw_stream(device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-class _On:
-    """``with _On(device)``: make it current, where it is not already."""
-
-    __slots__ = ("to", "back")
-
-    def __init__(self, device):
-        self.to = device.index
-
-    def __enter__(self):
-        now = torch._C._cuda_getDevice()
-        self.back = None if now == self.to else now
-        if self.back is not None:
-            torch.cuda.set_device(self.to)
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
 
 
 def _need_shape(t, name, shape, dtype, device, optional=False):
@@ -341,7 +322,7 @@ def _own_workspace(device, nbytes: int) -> torch.Tensor:
     capturing = torch.cuda.is_current_stream_capturing()
     if nbytes <= 256 and not capturing:
         return workspace_for(device)
-    stream = _raw_stream(device)
+    stream = _current_raw_stream(device.index)
     keep = nbytes <= _KEEP_BYTES and not capturing
     ws = _stream_workspaces.get((device.index, stream)) if keep else None
     if ws is None or ws.numel() < nbytes:
@@ -388,18 +369,20 @@ def gated_linear_attn_fwd(q, k, v, alpha=None, S0=None, o=None, S_out=None, work
     _need_shape(S0, "S0", (B, H, Dk, Dv), torch.float32, dev, True)
     _need_shape(o, "o", (B, H, T, Dv), dtype, dev, True)
     _need_shape(S_out, "S_out", (B, H, Dk, Dv), torch.float32, dev, True)
-    with _On(dev):
-        if o is None:
-            o = torch.empty_like(v)
-        if S_out is None:
-            S_out = torch.empty(B, H, Dk, Dv, dtype=torch.float32, device=dev)
-        if workspace is None:
-            ws = _own_workspace(dev, _gated_bytes("gated_linear_attn_workspace_bytes", B, H, T, Dk, Dv, dtype))
-        else:
-            ws = _need(workspace, "workspace", torch.uint8, dev)
-        check("gated_linear_attn_fwd", lib().gated_linear_attn_fwd(
-            _at(q), _at(k), _at(v), _at(alpha), _at(S0), _at(o), _at(S_out),
-            B, H, T, Dk, Dv, _DT[dtype], _at(ws), ws.numel(), _raw_stream(dev)))
+    if _current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return gated_linear_attn_fwd(q, k, v, alpha, S0, o, S_out, workspace)
+    if o is None:
+        o = torch.empty_like(v)
+    if S_out is None:
+        S_out = torch.empty(B, H, Dk, Dv, dtype=torch.float32, device=dev)
+    if workspace is None:
+        ws = _own_workspace(dev, _gated_bytes("gated_linear_attn_workspace_bytes", B, H, T, Dk, Dv, dtype))
+    else:
+        ws = _need(workspace, "workspace", torch.uint8, dev)
+    check("gated_linear_attn_fwd", lib().gated_linear_attn_fwd(
+        _at(q), _at(k), _at(v), _at(alpha), _at(S0), _at(o), _at(S_out),
+        B, H, T, Dk, Dv, _DT[dtype], _at(ws), ws.numel(), _current_raw_stream(dev.index)))
     return o, S_out
 
 
@@ -411,19 +394,21 @@ def gated_linear_attn_bwd(q, k, v, dO, alpha=None, S0=None, dS_T=None, workspace
     _need_shape(dO, "dO", (B, H, T, Dv), dtype, dev)
     for t, n in ((S0, "S0"), (dS_T, "dS_T")):
         _need_shape(t, n, (B, H, Dk, Dv), torch.float32, dev, True)
-    with _On(dev):
-        f = dict(dtype=torch.float32, device=dev)
-        out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
-                   dlog_alpha=None if alpha is None else torch.empty(B, H, T, **f),
-                   dS0=torch.empty(B, H, Dk, Dv, **f))
-        if workspace is None:
-            ws = _own_workspace(dev, _gated_bytes("gated_linear_attn_bwd_workspace_bytes", B, H, T, Dk, Dv, dtype))
-        else:
-            ws = _need(workspace, "workspace", torch.uint8, dev)
-        check("gated_linear_attn_bwd", lib().gated_linear_attn_bwd(
-            _at(q), _at(k), _at(v), _at(alpha), _at(S0), _at(dO), _at(dS_T), _at(out["dq"]),
-            _at(out["dk"]), _at(out["dv"]), _at(out["dlog_alpha"]), _at(out["dS0"]),
-            B, H, T, Dk, Dv, _DT[dtype], _at(ws), ws.numel(), _raw_stream(dev)))
+    if _current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return gated_linear_attn_bwd(q, k, v, dO, alpha, S0, dS_T, workspace)
+    f = dict(dtype=torch.float32, device=dev)
+    out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
+               dlog_alpha=None if alpha is None else torch.empty(B, H, T, **f),
+               dS0=torch.empty(B, H, Dk, Dv, **f))
+    if workspace is None:
+        ws = _own_workspace(dev, _gated_bytes("gated_linear_attn_bwd_workspace_bytes", B, H, T, Dk, Dv, dtype))
+    else:
+        ws = _need(workspace, "workspace", torch.uint8, dev)
+    check("gated_linear_attn_bwd", lib().gated_linear_attn_bwd(
+        _at(q), _at(k), _at(v), _at(alpha), _at(S0), _at(dO), _at(dS_T), _at(out["dq"]),
+        _at(out["dk"]), _at(out["dv"]), _at(out["dlog_alpha"]), _at(out["dS0"]),
+        B, H, T, Dk, Dv, _DT[dtype], _at(ws), ws.numel(), _current_raw_stream(dev.index)))
     return out
 
 
@@ -434,11 +419,13 @@ def gated_linear_attn_decode_step(q, k, v, S, alpha=None, o=None):
     dev, dtype, (B, H), Dk, Dv = _recurrence_inputs(q, k, v, alpha, 3)
     _need_shape(S, "S", (B, H, Dk, Dv), torch.float32, dev)
     _need_shape(o, "o", (B, H, Dv), dtype, dev, True)
-    with _On(dev):
-        if o is None:
-            o = torch.empty_like(v)
-        check("gated_linear_attn_decode_step", lib().gated_linear_attn_decode_step(
-            _at(q), _at(k), _at(v), _at(alpha), _at(S), _at(o), B, H, Dk, Dv, _DT[dtype], _raw_stream(dev)))
+    if _current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return gated_linear_attn_decode_step(q, k, v, S, alpha, o)
+    if o is None:
+        o = torch.empty_like(v)
+    check("gated_linear_attn_decode_step", lib().gated_linear_attn_decode_step(
+        _at(q), _at(k), _at(v), _at(alpha), _at(S), _at(o), B, H, Dk, Dv, _DT[dtype], _current_raw_stream(dev.index)))
     return o
 
 
@@ -452,7 +439,7 @@ def _need_rows(t, name, dtype=None, device=None):
         raise ValueError(f"{name} must have 4 dimensions (B,T,H,D), got {t.dim()}")
     if t.stride(3) != 1 and t.numel() > 0:
         raise ValueError(f"{name} must have contiguous rows")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
@@ -461,7 +448,9 @@ def _need_rows(t, name, dtype=None, device=None):
 
 def _row_strides(t):
     """Strides over b, t and h; an axis of one element or none has stride 0."""
-    return [s if n > 1 else 0 for s, n in zip(t.stride()[:3], t.shape[:3])]
+    sb, st, sh, _ = t.stride()
+    B, T, H, _ = t.shape
+    return sb if B > 1 else 0, st if T > 1 else 0, sh if H > 1 else 0
 
 
 def _qk_args(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, silu, interleaved):
@@ -512,15 +501,17 @@ def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, positions=None, inv_fre
         q, k, q_weight, k_weight, positions, inv_freq, norm, eps, silu, interleaved)
     _need_shape(q_out, "q_out", (B, Hq, T, D), dtype, dev, True)
     _need_shape(k_out, "k_out", (B, Hk, T, D), dtype, dev, True)
-    with _On(dev):
-        if q_out is None:
-            q_out = torch.empty(B, Hq, T, D, dtype=dtype, device=dev)
-        if k_out is None:
-            k_out = torch.empty(B, Hk, T, D, dtype=dtype, device=dev)
-        check("qk_norm_rope_fwd", lib().qk_norm_rope_fwd(
-            _at(q), _at(k), _at(q_weight), _at(k_weight), _at(positions), _at(inv_freq), _at(q_out),
-            _at(k_out), B, T, Hq, Hk, D, rot, *_row_strides(q), *_row_strides(k), ps, eps, opts, _DT[dtype],
-            _raw_stream(dev)))
+    if _current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, silu, interleaved, q_out, k_out)
+    if q_out is None:
+        q_out = torch.empty(B, Hq, T, D, dtype=dtype, device=dev)
+    if k_out is None:
+        k_out = torch.empty(B, Hk, T, D, dtype=dtype, device=dev)
+    check("qk_norm_rope_fwd", lib().qk_norm_rope_fwd(
+        _at(q), _at(k), _at(q_weight), _at(k_weight), _at(positions), _at(inv_freq), _at(q_out),
+        _at(k_out), B, T, Hq, Hk, D, rot, *_row_strides(q), *_row_strides(k), ps, eps, opts, _DT[dtype],
+        _current_raw_stream(dev.index)))
     return q_out, k_out
 
 
@@ -541,29 +532,32 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, positio
         raise TypeError(f"dq_out must be {dtype} or torch.float32, got {gdt}")
     _need_shape(dq_out, "dq_out", (B, Hq, T, D), gdt, dev)
     _need_shape(dk_out, "dk_out", (B, Hk, T, D), gdt, dev)
-    with _On(dev):
-        if dq is None:
-            dq = torch.empty(B, T, Hq, D, dtype=dtype, device=dev)
-        if dk is None:
-            dk = torch.empty(B, T, Hk, D, dtype=dtype, device=dev)
-        for t, n, like in ((dq, "dq", q), (dk, "dk", k)):
-            _need_rows(t, n, dtype, dev)
-            if t.shape != like.shape:
-                raise ValueError(f"{n} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
-        dw = [None if w is None else torch.empty(D, dtype=torch.float32, device=dev) for w in (q_weight, k_weight)]
-        ws = workspace
-        if ws is None and (q_weight is not None or k_weight is not None):
-            nb = lib().qk_norm_rope_bwd_workspace_bytes(B, T, Hq, Hk, D)
-            if nb == 0:
-                raise DeltaNetError("qk_norm_rope_bwd_workspace_bytes", _lib.DN_ERR_UNSUPPORTED)
-            ws = torch.empty(nb, dtype=torch.uint8, device=dev)
-        if ws is not None:
-            _need(ws, "workspace", torch.uint8, dev)
-        check("qk_norm_rope_bwd", lib().qk_norm_rope_bwd(
-            _at(q), _at(k), _at(dq_out), _at(dk_out), _at(q_weight), _at(k_weight), _at(positions),
-            _at(inv_freq), _at(dq), _at(dk), _at(dw[0]), _at(dw[1]), B, T, Hq, Hk, D, rot,
-            *_row_strides(q), *_row_strides(k), *_row_strides(dq), *_row_strides(dk), ps, eps, opts, _DT[dtype],
-            _DT[gdt], _at(ws), 0 if ws is None else ws.numel(), _raw_stream(dev)))
+    if _current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, positions, inv_freq, norm, eps, silu,
+                                    interleaved, dq, dk, workspace)
+    if dq is None:
+        dq = torch.empty(B, T, Hq, D, dtype=dtype, device=dev)
+    if dk is None:
+        dk = torch.empty(B, T, Hk, D, dtype=dtype, device=dev)
+    for t, n, like in ((dq, "dq", q), (dk, "dk", k)):
+        _need_rows(t, n, dtype, dev)
+        if t.shape != like.shape:
+            raise ValueError(f"{n} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    dw = [None if w is None else torch.empty(D, dtype=torch.float32, device=dev) for w in (q_weight, k_weight)]
+    ws = workspace
+    if ws is None and (q_weight is not None or k_weight is not None):
+        nb = lib().qk_norm_rope_bwd_workspace_bytes(B, T, Hq, Hk, D)
+        if nb == 0:
+            raise DeltaNetError("qk_norm_rope_bwd_workspace_bytes", _lib.DN_ERR_UNSUPPORTED)
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+    if ws is not None:
+        _need(ws, "workspace", torch.uint8, dev)
+    check("qk_norm_rope_bwd", lib().qk_norm_rope_bwd(
+        _at(q), _at(k), _at(dq_out), _at(dk_out), _at(q_weight), _at(k_weight), _at(positions),
+        _at(inv_freq), _at(dq), _at(dk), _at(dw[0]), _at(dw[1]), B, T, Hq, Hk, D, rot,
+        *_row_strides(q), *_row_strides(k), *_row_strides(dq), *_row_strides(dk), ps, eps, opts, _DT[dtype],
+        _DT[gdt], _at(ws), 0 if ws is None else ws.numel(), _current_raw_stream(dev.index)))
     return dict(dq=dq, dk=dk, dq_weight=dw[0], dk_weight=dw[1])
 
 
