@@ -17,6 +17,7 @@ library's CUDA kernels.  There is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import threading
 
 import torch
 
@@ -310,6 +311,7 @@ def _need_shape(t, name, shape, dtype, device, optional=False):
 
 
 _stream_workspaces: dict = {}
+_scratch_call = threading.Lock()  # a call's launches go together: threads may share a stream, and so its scratch
 _KEEP_BYTES = 32 << 20  # larger scratch is allocated for each call
 
 
@@ -376,13 +378,14 @@ def gated_linear_attn_fwd(q, k, v, alpha=None, S0=None, o=None, S_out=None, work
         o = torch.empty_like(v)
     if S_out is None:
         S_out = torch.empty(B, H, Dk, Dv, dtype=torch.float32, device=dev)
-    if workspace is None:
-        ws = _own_workspace(dev, _gated_bytes("gated_linear_attn_workspace_bytes", B, H, T, Dk, Dv, dtype))
-    else:
-        ws = _need(workspace, "workspace", torch.uint8, dev)
-    check("gated_linear_attn_fwd", lib().gated_linear_attn_fwd(
-        _at(q), _at(k), _at(v), _at(alpha), _at(S0), _at(o), _at(S_out),
-        B, H, T, Dk, Dv, _DT[dtype], _at(ws), ws.numel(), _current_raw_stream(dev.index)))
+    with _scratch_call:
+        if workspace is None:
+            ws = _own_workspace(dev, _gated_bytes("gated_linear_attn_workspace_bytes", B, H, T, Dk, Dv, dtype))
+        else:
+            ws = _need(workspace, "workspace", torch.uint8, dev)
+        check("gated_linear_attn_fwd", lib().gated_linear_attn_fwd(
+            _at(q), _at(k), _at(v), _at(alpha), _at(S0), _at(o), _at(S_out),
+            B, H, T, Dk, Dv, _DT[dtype], _at(ws), ws.numel(), _current_raw_stream(dev.index)))
     return o, S_out
 
 
@@ -401,14 +404,15 @@ def gated_linear_attn_bwd(q, k, v, dO, alpha=None, S0=None, dS_T=None, workspace
     out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
                dlog_alpha=None if alpha is None else torch.empty(B, H, T, **f),
                dS0=torch.empty(B, H, Dk, Dv, **f))
-    if workspace is None:
-        ws = _own_workspace(dev, _gated_bytes("gated_linear_attn_bwd_workspace_bytes", B, H, T, Dk, Dv, dtype))
-    else:
-        ws = _need(workspace, "workspace", torch.uint8, dev)
-    check("gated_linear_attn_bwd", lib().gated_linear_attn_bwd(
-        _at(q), _at(k), _at(v), _at(alpha), _at(S0), _at(dO), _at(dS_T), _at(out["dq"]),
-        _at(out["dk"]), _at(out["dv"]), _at(out["dlog_alpha"]), _at(out["dS0"]),
-        B, H, T, Dk, Dv, _DT[dtype], _at(ws), ws.numel(), _current_raw_stream(dev.index)))
+    with _scratch_call:
+        if workspace is None:
+            ws = _own_workspace(dev, _gated_bytes("gated_linear_attn_bwd_workspace_bytes", B, H, T, Dk, Dv, dtype))
+        else:
+            ws = _need(workspace, "workspace", torch.uint8, dev)
+        check("gated_linear_attn_bwd", lib().gated_linear_attn_bwd(
+            _at(q), _at(k), _at(v), _at(alpha), _at(S0), _at(dO), _at(dS_T), _at(out["dq"]),
+            _at(out["dk"]), _at(out["dv"]), _at(out["dlog_alpha"]), _at(out["dS0"]),
+            B, H, T, Dk, Dv, _DT[dtype], _at(ws), ws.numel(), _current_raw_stream(dev.index)))
     return out
 
 
@@ -503,7 +507,8 @@ def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, positions=None, inv_fre
     _need_shape(k_out, "k_out", (B, Hk, T, D), dtype, dev, True)
     if _current_device() != dev.index:
         with torch.cuda.device(dev):
-            return qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, silu, interleaved, q_out, k_out)
+            return qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, silu, interleaved,
+                                    q_out, k_out)
     if q_out is None:
         q_out = torch.empty(B, Hq, T, D, dtype=dtype, device=dev)
     if k_out is None:
@@ -569,9 +574,10 @@ def deltanet_get_device_status(device=None, workspace=None) -> int:
     status = lib().deltanet_get_device_status(_ptr(ws), _stream(device))
     if workspace is None and status == 0 and _stream_workspaces:
         index = torch.cuda.current_device() if device.index is None else device.index
-        for (i, stream), kept in list(_stream_workspaces.items()):
+        torch.cuda.synchronize(index)  # their streams may be gone by now
+        for (i, _), kept in list(_stream_workspaces.items()):
             if i == index and status == 0:
-                status = lib().deltanet_get_device_status(_ptr(kept), stream)
+                status = lib().deltanet_get_device_status(_ptr(kept), _stream(device))
     return status
 
 

@@ -438,6 +438,42 @@ bool rows_apart(int B, int T, int H, int D, long long sb, long long st, long lon
   return true;
 }
 
+// True if rows of two strided outputs whose bases are `delta` elements apart
+// share no element.  Each is rows_apart, and along an axis that both have they
+// step alike (otherwise false: such a pair is told apart by whole ranges
+// alone).  They meet where the sum of (index difference) * stride comes within
+// D of delta; from the widest axis down only the two multiples around what is
+// left can, since the axes below together move by less than one step.
+struct DeltaAxis {
+  long long stride, lo, hi;  // index differences of k's row and q's row
+};
+bool meets(const DeltaAxis* ax, int n, long long left, int D) {
+  if (n == 0) return left > -D && left < D;
+  long long c = left / ax->stride;
+  if (c * ax->stride > left) --c;
+  for (long long x = c; x <= c + 1; ++x)
+    if (x >= ax->lo && x <= ax->hi && meets(ax + 1, n - 1, left - x * ax->stride, D)) return true;
+  return false;
+}
+bool tensors_apart(const dn::QkProblem& p, long long delta) {
+  if ((p.B > 1 && p.dqs_b != p.dks_b) || (p.T > 1 && p.dqs_t != p.dks_t) ||
+      (p.Hq > 1 && p.Hk > 1 && p.dqs_h != p.dks_h))
+    return false;
+  DeltaAxis ax[3];
+  int n = 0;
+  if (p.B > 1) ax[n++] = {p.dqs_b, 1 - p.B, p.B - 1};
+  if (p.T > 1) ax[n++] = {p.dqs_t, 1 - p.T, p.T - 1};
+  if (p.Hq > 1 || p.Hk > 1) ax[n++] = {p.Hq > 1 ? p.dqs_h : p.dks_h, 1 - p.Hq, p.Hk - 1};
+  for (int i = 0; i < n; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (ax[j].stride > ax[i].stride) {
+        const DeltaAxis x = ax[i];
+        ax[i] = ax[j];
+        ax[j] = x;
+      }
+  return !meets(ax, n, -delta, p.D);
+}
+
 }  // namespace
 
 extern "C" {
@@ -672,6 +708,9 @@ int qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const voi
     for (const Range& x : rest)
       if (rc == DN_OK && overlap(r, x)) rc = DN_ERR_INVALID_ARG;
   }
+  if (rc == DN_OK && rows && overlap(range_of(dq, sq), range_of(dk, sk)) &&
+      !tensors_apart(p, (long long)((intptr_t)dk - (intptr_t)dq) / (long long)es))
+    rc = DN_ERR_INVALID_ARG;
   if (rc != DN_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   if (!rows) {  // sums over nothing

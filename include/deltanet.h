@@ -316,7 +316,7 @@ int deltanet_chunk_bwd(const void *q, const void *k, const void *v,
  * The sizes depend on the current device's SM count, which must be that of the
  * call.  Arithmetic: bf16 inputs run on tensor cores with float32 accumulation
  * and state (products with rounded operands: the decayed scores and the state
- * that o reads; the state itself carries about 17 bits more than bf16);
+ * that o reads; the state itself is carried to about 17 bits);
  * float32 inputs run in float32.  The result is deterministic.  A NaN or Inf
  * in q, k or v reaches, beside what the recurrence itself spreads it to, the
  * other tokens of its chunk (at most 128 tokens) of the same (b, h).
@@ -396,8 +396,9 @@ int qk_norm_rope_fwd(const void *q, const void *k, const float *q_weight, const 
  * Gradient of qk_norm_rope_fwd.  dq_out (B,Hq,T,D) and dk_out (B,Hk,T,D) are
  * the derivatives by its outputs, of element type grad_dt: dt, or float32 (what
  * deltanet_chunk_bwd writes).  dq and dk take the derivatives by q and k, of
- * element type dt, by strides of their own (a fused gradient's slices, say;
- * rows that overlap one another are rejected).  dq_weight, dk_weight: (D)
+ * element type dt, by strides of their own (a fused gradient's slices, say:
+ * with equal strides they may lie among one another; rows that share an
+ * element are rejected).  dq_weight, dk_weight: (D)
  * float32, NULL where not wanted or where the weight is NULL; summed over all
  * rows in a fixed order (deterministic).  workspace:
  * qk_norm_rope_bwd_workspace_bytes(...) bytes, 16-byte aligned, needs no

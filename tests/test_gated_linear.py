@@ -491,6 +491,45 @@ def test_streams_and_graphs(dn, T):
 
 
 @gpu
+def test_threads_on_one_stream(dn):
+    """Threads that share a stream share its scratch too: a call's launches stay together."""
+    import threading
+
+    xs = [case(1, 2, 3000, 64, 64, torch.bfloat16, seed=s) for s in range(4)]
+    run = lambda x: (*dn.gated_linear_attn_fwd(*pick(x, FWD)), *dn.gated_linear_attn_bwd(*pick(x, BWD)).values())
+    want = [run(x) for x in xs]
+    bad = []
+
+    def work(i):
+        for _ in range(30):
+            if not all(torch.equal(a, b) for a, b in zip(run(xs[i]), want[i])):
+                bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+@gpu
+def test_status_after_a_stream_is_gone(dn):
+    import gc
+
+    x = case(1, 2, 3000, 64, 64, torch.bfloat16, seed=1)
+    want = dn.gated_linear_attn_fwd(*pick(x, FWD))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = dn.gated_linear_attn_fwd(*pick(x, FWD))
+    del s
+    gc.collect()
+    assert dn.deltanet_get_device_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@gpu
 def test_binding_refusals(dn):
     x = case(1, 2, 8, 64, 64, torch.bfloat16)
     bad = [dict(k=x["k"][:, :, :4].contiguous()), dict(v=x["v"].float()), dict(alpha=x["alpha"][:, :1].contiguous()),

@@ -170,6 +170,27 @@ def test_bwd_refusals(L):
     assert call(dwq=A + 200 * MB) == E.DN_ERR_INVALID_ARG  # a weight's gradient in the workspace
 
 
+def test_bwd_refuses_dq_and_dk_on_one_another(L):
+    from deltanet_sequence_mixing_b200 import _lib as E
+
+    def call(delta, s, B=2, T=10, Hq=2, Hk=2, sk=None):
+        in_s = [T * Hq * 64, Hq * 64, 64, T * Hk * 64, Hk * 64, 64]
+        return L.qk_norm_rope_bwd(vp(A), vp(A + 16 * MB), vp(A + 96 * MB), vp(A + 112 * MB), None, None, None,
+                                  vp(A + 36 * MB), vp(A + 64 * MB), vp(A + 64 * MB + 2 * delta), None, None, B, T,
+                                  Hq, Hk, 64, 64, *in_s, *s, *(sk or s), 0, 1e-6, 0, 1, 1, None, 0, None)
+
+    bad = E.DN_ERR_INVALID_ARG
+    assert call(0, [1280, 128, 64]) == bad  # one tensor
+    assert call(256, [1280, 128, 64]) == bad  # two tokens on
+    assert call(-1280, [1280, 128, 64]) == bad  # one sequence back
+    assert call(64, [5120, 512, 64]) == bad  # k's first head on q's second
+    assert call(128, [5120, 512, 64], Hq=3) == bad
+    assert call(512 + 64, [5120, 512, 64]) == bad  # the same in the next token
+    assert call(32, [2560, 256, 64], Hq=1, Hk=1) == bad  # half a row
+    assert call(128, [2560, 256, 64], sk=[2560, 128, 64]) == bad  # strides of their own in one range
+    assert call(640 + 64, [2560, 64, 640]) == bad  # heads outside tokens
+
+
 def test_binding_refuses_host_tensors():
     import deltanet_sequence_mixing_b200 as m
 
@@ -233,6 +254,30 @@ def test_strides_and_slices_of_one_gradient(dn):
     # one row of q and k for every head (a broadcast input): each head's gradient apart
     one = q[:, :, :1].expand(2, 20, 3, 64)
     check(dn, one, k, wq, wk, pos, freq, grads)
+
+
+@gpu
+@pytest.mark.parametrize("B,T,Hq,Hk", [(2, 20, 3, 3), (2, 20, 1, 4), (1, 20, 4, 1), (3, 1, 2, 5)])
+@pytest.mark.parametrize("axis", [1, 2, 3, 4])
+def test_gradients_side_by_side(dn, B, T, Hq, Hk, axis):
+    """dq and dk in one buffer: q's heads in front of k's, heads inside or outside
+    the tokens (axis 2, 1); with as many of both, in pairs (3) or k's in front (4)."""
+    if axis >= 3 and Hq != Hk:
+        Hk = Hq
+    q, k, wq, wk, pos, freq, grads = case(B, T, Hq, Hk, 64, torch.bfloat16, 64, 21)
+    if axis == 1:
+        buf = torch.full((B, Hq + Hk + 1, T, 64), 7.0, dtype=torch.bfloat16, device="cuda").transpose(1, 2)
+    else:
+        buf = torch.full((B, T, Hq + Hk + 1, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    dq, dk = buf[:, :, 1:1 + Hq], buf[:, :, 1 + Hq:]
+    if axis == 3:
+        dq, dk = buf[:, :, 1::2], buf[:, :, 2::2]
+    if axis == 4:
+        dq, dk = buf[:, :, 1 + Hq:], buf[:, :, 1:1 + Hq]
+    want = dn.qk_norm_rope_bwd(q, k, *grads, wq, wk, pos, freq)
+    got = dn.qk_norm_rope_bwd(q, k, *grads, wq, wk, pos, freq, dq=dq, dk=dk)
+    assert all(torch.equal(got[n], want[n]) for n in want)
+    assert bool((buf[:, :, 0] == 7).all())
 
 
 @gpu
