@@ -360,9 +360,9 @@ int validate_gated_sizes(int B, int H, int T, int Dk, int Dv, int dt) {
   return DN_OK;
 }
 
-// The segments of a bf16 call on the current device.
-void gated_split(int B, int H, int T, int Dv, int* G, int* seg_chunks) {
-  dn::gated_segments(B * H, T, Dv, sm_count_now(), G, seg_chunks);
+// The segments of a bf16 call on the current device, its scans side by side.
+void gated_split(int B, int H, int T, int Dv, int directions, int* G, int* seg_chunks) {
+  dn::gated_segments(B * H, T, Dv, sm_count_now(), directions, G, seg_chunks);
 }
 
 // The state of the sequence's end when there are no tokens.
@@ -485,7 +485,7 @@ size_t gated_linear_attn_workspace_bytes(int B, int H, int T, int Dk, int Dv, dn
     return kStatusBytes +
            (dn::gated_simt_walks(B * H, T, Dv, sm_count_now()) ? 0 : dn::gated_simt_bytes(B * H, T, Dk, Dv, 1));
   int G, per;
-  gated_split(B, H, T, Dv, &G, &per);
+  gated_split(B, H, T, Dv, 1, &G, &per);
   return kStatusBytes + dn::gated_segment_bytes(B * H, G, Dk, Dv);
 }
 
@@ -520,7 +520,7 @@ int gated_linear_attn_fwd(const void* q, const void* k, const void* v, const flo
     if (dn::gated_simt_walks(B * H, T, Dv, sm_count_now())) p.scratch = nullptr;
     return map_cuda(dn::launch_gated_simt_fwd(p, st));
   }
-  gated_split(B, H, T, Dv, &p.G, &p.seg_chunks);
+  gated_split(B, H, T, Dv, 1, &p.G, &p.seg_chunks);
   return map_cuda(dn::launch_gated_tc_fwd(p, st));
 }
 
@@ -529,7 +529,7 @@ size_t gated_linear_attn_bwd_workspace_bytes(int B, int H, int T, int Dk, int Dv
   if ((long long)B * H == 0 || T == 0) return kStatusBytes;
   if (dt == DN_BF16) {
     int G, per;
-    gated_split(B, H, T, Dv, &G, &per);
+    gated_split(B, H, T, Dv, 2, &G, &per);
     return kStatusBytes + dn::gated_bwd_bytes(B * H, T, G, Dk, Dv);
   }
   return kStatusBytes + dn::gated_simt_bytes(B * H, T, Dk, Dv, 2);
@@ -574,7 +574,7 @@ int gated_linear_attn_bwd(const void* q, const void* k, const void* v, const flo
   p.status = static_cast<unsigned int*>(workspace);
   p.scratch = static_cast<uint8_t*>(workspace) + kStatusBytes;
   if (!p.bf16) return map_cuda(dn::launch_gated_simt_bwd(p, st));
-  gated_split(B, H, T, Dv, &p.G, &p.seg_chunks);
+  gated_split(B, H, T, Dv, 2, &p.G, &p.seg_chunks);
   p.sms = sm_count_now();
   return map_cuda(dn::launch_gated_tc_bwd(p, st));
 }

@@ -4,7 +4,9 @@
 // Bound by HBM: each Dk x Dv float32 state is read once and written once.  No
 // reduction stands between the read and the write (the delta rule's step has
 // one), so a state may be cut into column slices that never meet: one CTA
-// takes NC columns of one head.
+// takes NC columns of one head.  256 x 32 states of 128 x 128: 160 us, 6.7 TB/s;
+// one sequence of 16 heads: 1.7 us.  Slices of 16 columns take 162 and 1.65 us
+// there (5.5 us for 4.2 at 8 x 32 states), slices of 64 158 and 2.1 us.
 #include <cuda_bf16.h>
 
 #include "kernels.h"

@@ -30,7 +30,10 @@
 //   warps 16-19  O (c) = G_i QS + PV
 // C = 128 and full-height MMAs because an SS product of M = 128 reads 4 KB of A
 // for every 16 of K whatever N is: larger chunks spread the state's products
-// over more tokens, and shared-memory bandwidth is what the kernel spends.
+// over more tokens, and shared-memory bandwidth is what the kernel spends (the
+// operands, the tiles in and the scaling are 2700 of a chunk's 3400 cycles).  B4
+// H16 T4096 D128: 64 to 68 us for 274 MB (41 us at a copy's rate).  32 warps of
+// 64 registers instead of 20 took 83 us where these took 78.
 //
 // A long sequence over few heads is cut into G segments: a first launch of the
 // state part alone (from zero, K and V only) leaves every segment's end state
@@ -54,7 +57,7 @@ static_assert(C == 128, "four warps of 32 rows");
 constexpr uint32_t kBlk = 16384;  // 128 rows x 128 bytes (64 bf16 columns)
 constexpr int kWarpTma = 0, kWarpMma = 1, kWarpMma2 = 2, kWarpDecay = 3, kWarpP = 4, kWarpState = 12, kWarpO = 16;
 constexpr int kThreads = 20 * 32;
-constexpr int kBarS = 1;
+constexpr int kBarS = 1, kBarJoin = 2;
 // TMEM columns: scores [2] (P's halves in columns 0-31 and 64-95 of them), increment hi | lo, Q S, P V
 constexpr uint32_t TM_SC = 0, TM_DS = 256, TM_QS = 384, TM_PV = 448;
 
@@ -199,16 +202,17 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return r;
 }
 // 32 bytes to global memory, past L1 and in one instruction where they are
-// 32-byte aligned (whole sectors).  B4 H16 T4096 D128 forward: 68 us so, 78 us
-// with room made in L1, 85 us in 16-byte stores.
+// 32-byte aligned (whole sectors).  B4 H16 T4096 D128 forward: 64 to 68 us so, 78
+// with room made in L1, 85 in 16-byte stores.
 __device__ __forceinline__ void st_global32(void* dst, const uint32_t* r, bool wide) {
   if (!wide) {
     reinterpret_cast<uint4*>(dst)[0] = make_uint4(r[0], r[1], r[2], r[3]);
     reinterpret_cast<uint4*>(dst)[1] = make_uint4(r[4], r[5], r[6], r[7]);
     return;
   }
-  asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(reinterpret_cast<uint64_t>(dst)), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+  asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(
+                   reinterpret_cast<uint64_t>(dst)),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
 
@@ -227,8 +231,8 @@ __device__ __forceinline__ void split8(const float* x, uint4& hi, uint4& lo) {
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// 16-byte pieces [c0, c1) of row `row` of a 64-column tile, scaled by f into the hi and lo tiles, in bf16
-// arithmetic: with f = f_hi + f_lo (bf16 each, 2^-17 left behind), hi = v f_hi
+// 16-byte pieces [c0, c1) of row `row` of a 64-column tile, scaled by f into the
+// hi and lo tiles, in bf16 arithmetic: with f = f_hi + f_lo (bf16 each, 2^-17 left behind), hi = v f_hi
 // rounded, v f_hi - hi fits bf16 exactly (a product of two 8-bit significands
 // has 16 bits), and lo = that + v f_lo: three instructions for two values.
 __device__ __forceinline__ void scale_row(const uint8_t* tile, uint8_t* hi, uint8_t* lo, int row, float f, int c0,
@@ -258,26 +262,33 @@ __device__ __forceinline__ void scale_row(const uint8_t* tile, uint8_t* hi, uint
   }
 }
 
+// Where columns [col, col + 4) of row `row` of segment u's end state lie: four
+// columns of all rows together, so that a warp's 32 rows are 512 bytes in a row
+// (by rows, every lane a line of its own, a segment took 1 us to enter).
+template <int DK>
+__device__ __forceinline__ float4* segment_at(const GatedScan& p, size_t u, int col, int row) {
+  return reinterpret_cast<float4*>(p.seg_end + u * DK * p.Dv) + (size_t)(col / 4) * DK + row;
+}
 // NC columns of this thread's state row, entering segment g: the caller's
 // state and the segments passed before it in the scan's direction.
 template <int DK, int NC>
 __device__ __forceinline__ void enter_state(const GatedScan& p, bool rev, size_t bh, int g, int j0, int row,
                                             float (&s)[NC]) {
-  const size_t sblk = (size_t)DK * p.Dv, at = (size_t)row * p.Dv + j0;
-  const float* src = p.S_in ? p.S_in + bh * p.S_in_stride + at : nullptr;
+  const float* src = p.S_in ? p.S_in + bh * p.S_in_stride + (size_t)row * p.Dv + j0 : nullptr;
 #pragma unroll
   for (int j = 0; j < NC; j += 4) {
     const float4 v = src ? *reinterpret_cast<const float4*>(src + j) : make_float4(0.f, 0.f, 0.f, 0.f);
     s[j] = v.x; s[j + 1] = v.y; s[j + 2] = v.z; s[j + 3] = v.w;
   }
   const int n = rev ? p.G - 1 - g : g;
+#pragma unroll 2
   for (int i = 0; i < n; ++i) {
     const size_t u = bh * p.G + (rev ? p.G - 1 - i : i);
-    const float gam = p.seg_decay[u];
-    const float4* e = reinterpret_cast<const float4*>(p.seg_end + u * sblk + at);
+    const float gam = __ldg(p.seg_decay + u);
+    const float4* e = segment_at<DK>(p, u, j0, row);
 #pragma unroll
     for (int j = 0; j < NC; j += 4) {
-      const float4 v = __ldg(e + j / 4);
+      const float4 v = __ldg(e + (size_t)(j / 4) * DK);
       s[j] = fmaf(gam, s[j], v.x);
       s[j + 1] = fmaf(gam, s[j + 1], v.y);
       s[j + 2] = fmaf(gam, s[j + 2], v.z);
@@ -368,6 +379,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(bar + b + 8 * (c & 1));
   };
 
+  // The state that a later segment is entered with: sixteen warps take as many
+  // columns of it each and pass them to the state's warps in V~'s place, which
+  // the scaling warps leave alone until then.  (The state's four warps alone
+  // took 1.2 us for every segment before theirs.)
+  const bool joined = g > 0;
+  auto passed = [&](int col, int row) {
+    return reinterpret_cast<float4*>(sm + L::VT_OFF) + (size_t)(col / 4) * DK + row;
+  };
+  if (joined && warp >= kWarpP) {
+    const int row = 32 * w + lane, col = 16 * ((warp - kWarpP) >> 2);
+    if (row < DK) {
+      float s[16];
+      enter_state<DK>(p, false, bh, g, j0 + col, row, s);
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) *passed(col + j, row) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+    }
+    named_bar_sync(kBarS, 512);
+  }
+
   if (warp == kWarpTma) {
     // ------------------------------------------------------------------ TMA --
     if (lane == 0) {
@@ -438,7 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dv = desc_mn(sb + L::V_OFF + (c % 3) * kBlk, kBlk);
 #pragma unroll 2
       for (int ks = 0; ks < C / 16; ++ks)
-        mma_bf16_ts_elect(tmem + TM_PV, tmem + TM_SC + 128 * (c & 1) + 64 * (ks >> 2) + 8 * (ks & 3), desc_step(dv, ks * 2048), id, ks > 0);
+        mma_bf16_ts_elect(tmem + TM_PV, tmem + TM_SC + 128 * (c & 1) + 64 * (ks >> 2) + 8 * (ks & 3),
+                          desc_step(dv, ks * 2048), id, ks > 0);
       mma_commit_elect(bar + B_PV + 8 * (c & 1));
       mma_commit_elect(bar + B_VFREE + 8 * (c % 3));
     };
@@ -501,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return GATED && c < n && t < T ? __ldg(alpha + t) : 1.f;
     };
     ahead = load(0);
+    if (GATED && joined) named_bar_sync(kBarJoin, 384);
     bool ok = true;
     for (int c = 0; c < n && ok; ++c) {
       const float a = ahead, pre = GATED ? prefix_product(a) : 1.f;
@@ -578,7 +610,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     float s[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) s[j] = 0.f;
-    if (live) enter_state<DK>(p, false, bh, g, j0, row, s);
+    if (joined && live) {
+#pragma unroll
+      for (int j = 0; j < NV; j += 4) {
+        const float4 v = *passed(j, row);
+        s[j] = v.x; s[j + 1] = v.y; s[j + 2] = v.z; s[j + 3] = v.w;
+      }
+    } else if (live && p.S_in) {
+      const float* src = p.S_in + bh * p.S_in_stride + (size_t)row * p.Dv + j0;
+#pragma unroll
+      for (int j = 0; j < NV; j += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src + j);
+        s[j] = v.x; s[j + 1] = v.y; s[j + 2] = v.z; s[j + 3] = v.w;
+      }
+    }
+    if (GATED && joined) named_bar_sync(kBarJoin, 384);
     auto put = [&]() {
       if (live) {
 #pragma unroll
@@ -667,7 +713,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // state in the scan's direction as bf16 hi and lo, from the segment's true entry
 // (STORE).  With the scaled Z twice, scaling a chunk runs beside the products of
 // the one before; what is left is bound by what a chunk moves through shared
-// memory (copies in and out, the scaled Z, the operands).
+// memory (copies in and out, the scaled Z, the operands).  Both scans of B4 H16
+// T4096 D128 with their 537 MB: 105 us (82 at a copy's rate; 2 x 48 as two
+// launches of one scaled copy each, 110 as two CTAs of 64-token halves on an SM).
 constexpr int kStateThreads = 20 * 32;  // TMA 0, MMA 1, state 4-11, scaling 12-19
 template <int DK, bool GATED, bool STORE>
 __global__ void __launch_bounds__(kStateThreads, 1)
@@ -814,7 +862,9 @@ __global__ void __launch_bounds__(kStateThreads, 1)
       if (STORE) {
         if (p.S_out && g == (rev ? 0 : p.G - 1)) leave_state(p.S_out + (size_t)bh * sblk + at, s);
       } else {
-        leave_state(p.seg_end + ((size_t)bh * p.G + g) * sblk + at, s);
+        float4* e = segment_at<DK>(p, (size_t)bh * p.G + g, jc, row);
+#pragma unroll
+        for (int j = 0; j < NV / 2; j += 4) e[(size_t)(j / 4) * DK] = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
         if (leader && slice == 0) p.seg_decay[(size_t)bh * p.G + g] = total;
       }
     }
@@ -864,6 +914,12 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 // last gradients are made and stored.  Every barrier completes once a chunk.
 //   warp 0 TMA, warp 1 MMA, warps 4-11 epilogues (two warps to 32 rows, each
 //   half of the columns), warps 12-19 <S, R> (R in registers) and the sums
+//
+// B4 H16 T4096 D128, the scans included: 251 us (floor 72: the inputs and
+// gradients once).  A chunk's 352 KB in and out take 60% of it and the epilogues
+// of A, B and M most of the rest; the two overlap by the loads ahead.  Gradients
+// stored from registers took 275 us, the products with R first 268 to 282, heads
+// in batches to keep the states in L2 277.
 constexpr int kGradThreads = 20 * 32, kGradPlain = 12 * 32, kBarE = 1, kBarT = 2;
 enum : uint32_t {  // mbarriers, 8 bytes each
   G_QK = 0, G_VO = 8, G_RH = 16, G_RL = 24, G_SH = 32, G_SL = 40,               // loaded
@@ -1237,8 +1293,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t at = (uint32_t)half * kBlk + sw128_off(row, 2 * pc + h);
-            *reinterpret_cast<uint4*>(sm + L::PA_OFF + at) = make_uint4(pa[4 * h], pa[4 * h + 1], pa[4 * h + 2], pa[4 * h + 3]);
-            *reinterpret_cast<uint4*>(sm + L::PB_OFF + at) = make_uint4(pb[4 * h], pb[4 * h + 1], pb[4 * h + 2], pb[4 * h + 3]);
+            *reinterpret_cast<uint4*>(sm + L::PA_OFF + at) =
+                make_uint4(pa[4 * h], pa[4 * h + 1], pa[4 * h + 2], pa[4 * h + 3]);
+            *reinterpret_cast<uint4*>(sm + L::PB_OFF + at) =
+                make_uint4(pb[4 * h], pb[4 * h + 1], pb[4 * h + 2], pb[4 * h + 3]);
           }
         }
         tc_fence_before();
@@ -1256,7 +1314,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       }
       if (ok) {
         tc_fence_after();
-        esum = grad_row<DK / 2, GATED>(lanes + TG_C, lanes + TG_B, out, sm + L::K_OFF, sm + L::K_OFF, row, half * (DK / 2));
+        esum = grad_row<DK / 2, GATED>(lanes + TG_C, lanes + TG_B, out, sm + L::K_OFF, sm + L::K_OFF, row,
+                                       half * (DK / 2));
         store(&tmDK, L::K_OFF, KB);
         if (leader) {
           bulk_wait_group_read<1>();
@@ -1513,20 +1572,28 @@ cudaError_t launch_gated_tc_bwd(const GatedProblem& p, cudaStream_t st) {
   return p.Dk == 128 ? bwd<128, false>(p, st) : bwd<64, false>(p, st);
 }
 
-// Segments: enough for one CTA on every SM, where the state part run twice
-// (about half a chunk's cost each time, and some three chunks of launch and
-// entry) costs less than the chunks it takes off the longest chain.
-void gated_segments(int BH, int T, int Dv, int sms, int* G, int* seg_chunks) {
+// Segments: as many as there are SMs for, no more than 3 sqrt(chunks) (each
+// costs the later ones an entry), and none where the pass over their states
+// costs more than it takes off the longest chain.  In us, measured with Dk = Dv
+// = 128 for one head to 32 over 1024 to 65536 tokens: the forward 1.73 a chunk
+// in one chain, or 2.7 a chunk of a segment + 0.25 a segment + 5; the
+// gradient's scans 1.04, or 2.1 + 0.4 a segment + 3.  (B1 H1 T8192: forward in
+// one chain 114, in 8 | 16 | 32 | 64 segments 35 | 27 | 26 | 31, gradient 84, in
+// 8 | 16 | 32 | 64 41 | 36 | 39 | 51.  B1 H32: 2 segments at T8192 108 for 119,
+// at T2048 38 for 37; the gradient of H16 T8192 in 2 segments 169 for 165.)
+void gated_segments(int BH, int T, int Dv, int sms, int directions, int* G, int* seg_chunks) {
   const int nch = (T + C - 1) / C;
-  const long long ctas = (long long)BH * (Dv / NV);
+  const long long ctas = (long long)BH * (Dv / NV) * directions;
   *G = 1;
   *seg_chunks = nch;
   if (ctas < 1 || sms < 2 * ctas) return;
-  const int g = (int)(sms / ctas);
-  const int per = (nch + g - 1) / g;
-  if (2 * nch <= 3 * per + 6) return;
-  *seg_chunks = per;
-  *G = (nch + per - 1) / per;
+  long long g = sms / ctas;
+  while (g * g > 9LL * nch) --g;
+  if (g < 2) return;
+  const long long per = (nch + g - 1) / g, n = (nch + per - 1) / per;
+  if (directions == 1 ? 7LL * nch <= 11 * per + n + 24 : 5LL * nch <= 10 * per + 2 * n + 20) return;
+  *seg_chunks = (int)per;
+  *G = (int)n;
 }
 
 size_t gated_segment_bytes(int BH, int G, int Dk, int Dv) {

@@ -166,12 +166,12 @@ struct GatedScan {
   size_t S_in_stride;     // floats from one (b, h) to the next
   float* S_out;           // state leaving it, nullable
   float* seg_decay;       // [BH][G] product of alpha over a segment
-  float* seg_end;         // [BH][G][Dk][Dv] a segment's end state from zero
+  float* seg_end;         // [BH][G][Dv / 4][Dk][4] a segment's end state from zero
   unsigned int* status;
   int T, Dv, G, seg_chunks;
 };
 // The split of T into G segments of seg_chunks chunks (the last may be shorter).
-void gated_segments(int BH, int T, int Dv, int sms, int* G, int* seg_chunks);
+void gated_segments(int BH, int T, int Dv, int sms, int directions, int* G, int* seg_chunks);
 size_t gated_segment_bytes(int BH, int G, int Dk, int Dv);
 // Scratch of the bf16 gradient.
 size_t gated_bwd_bytes(int BH, int T, int G, int Dk, int Dv);

@@ -308,6 +308,20 @@ def test_long_sequences(dn, B, H, T):
 
 
 @gpu
+@pytest.mark.parametrize("gate", [None, "wipes"])
+@pytest.mark.parametrize("B,H,T,Dk,Dv", [(1, 1, 4100, 64, 128), (1, 2, 1500, 128, 64), (3, 3, 6000, 64, 64)])
+def test_segments_enter_in_place(dn, gate, B, H, T, Dk, Dv):
+    """Long sequences over few heads, whose parts start from the states of the
+    parts before them, with S_out on S0."""
+    x = case(B, H, T, Dk, Dv, torch.bfloat16, gate, seed=T)
+    o, S = check_fwd(dn, x, torch.bfloat16)
+    check_bwd(dn, x, torch.bfloat16)
+    S0 = x["S0"].clone()
+    o2, S2 = dn.gated_linear_attn_fwd(*pick(x, FWD[:4]), S0, S_out=S0)
+    assert S2 is S0 and torch.equal(o, o2) and torch.equal(S, S2)
+
+
+@gpu
 def test_many_heads(dn):
     x = case(8, 40, 150, 64, 64, torch.bfloat16, "mixed", True, 9)
     check_fwd(dn, x, torch.bfloat16)
