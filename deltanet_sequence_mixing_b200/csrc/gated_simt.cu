@@ -31,7 +31,7 @@
 //
 // Bound by the products' shared-memory operands and their multiply-adds (float32
 // has no tensor path); short sequences by the launches.  The gradient of a
-// ragged B2 H6 T777 Dk 64 Dv 128 takes 66 us, the forward of B1 H4 T100 D64 19 us.
+// ragged B2 H3 T777 Dk 128 Dv 64 takes 66 us, the forward of B1 H4 T100 D64 19 us.
 #include "kernels.h"
 
 namespace dn {

@@ -1326,7 +1326,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       }
       if (ok) {
         tc_fence_after();
-        fsum += grad_row<DK / 2, GATED>(lanes + TG_D, lanes + TG_A, into, sm + L::Q_OFF, sm + L::Q_OFF, row, half * (DK / 2));
+        fsum += grad_row<DK / 2, GATED>(lanes + TG_D, lanes + TG_A, into, sm + L::Q_OFF, sm + L::Q_OFF, row,
+                                        half * (DK / 2));
         tc_fence_before();
         arrive(G_ENDFREE);
         if (GATED) {  // B has been read: its place takes the sums
