@@ -23,8 +23,9 @@
 // then sine and cosine in float32: exact to float32 at any position.  A CTA
 // computes them once for a token and uses them for all of its heads.
 // B4 T4096 H16 D128 in bf16, full rotation: forward 56 us (4.8 TB/s), gradient 92
-// us (4.4 TB/s); beside the rows' traffic both issue near one instruction a cycle
-// and scheduler, so more loads in flight gained nothing.
+// us (4.4 TB/s).  What is left is the latency of the loads that 32 warps of an SM
+// have in flight (32 KB) and half of the issue slots: loads a row ahead took the
+// registers of as many warps and gained nothing.
 #include <cuda_bf16.h>
 
 #include <type_traits>
