@@ -638,7 +638,8 @@ size_t qk_norm_rope_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int D) {
       (long long)Hq + Hk > INT_MAX / 16)
     return 0;
   if (B == 0 || T == 0 || Hq + Hk == 0) return 16;  // nothing to add up, still a buffer
-  return (size_t)dn::qk_bwd_ctas(B, T, Hq, Hk, 0) * 2 * D * 4;
+  const int a = dn::qk_bwd_ctas(B, T, Hq, Hk, 0), b = dn::qk_bwd_ctas(B, T, Hq, Hk, 1);
+  return (size_t)(a > b ? a : b) * 2 * D * 4;
 }
 
 int qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, const float* q_weight,

@@ -22,8 +22,8 @@
 // Angles: position * inv_freq in float64, in turns, its whole part dropped,
 // then sine and cosine in float32: exact to float32 at any position.  A CTA
 // computes them once for a token and uses them for all of its heads.
-// B4 T4096 H16 D128 in bf16, full rotation: forward 56 us (4.8 TB/s), gradient 92
-// us (4.4 TB/s).  What is left is the latency of the loads that 32 warps of an SM
+// B4 T4096 H16 D128 in bf16, full rotation: forward 54 us (5 TB/s), gradient 90 us
+// (4.5 TB/s).  What is left is the latency of the loads that 32 warps of an SM
 // have in flight (32 KB) and half of the issue slots: loads a row ahead took the
 // registers of as many warps and gained nothing.
 #include <cuda_bf16.h>
@@ -208,7 +208,7 @@ struct Walk {
 };
 
 template <typename TI, int D, bool INTER, bool L2, bool SILU>
-__global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkProblem p, int tokens) {
+__global__ void __launch_bounds__(kThreads, 4) qk_fwd_kernel(const QkProblem p, int tokens) {
   constexpr int L = D / 16, ROWS = kThreads / L;
   extern __shared__ float turns[];
   __shared__ Tile tile[2];
@@ -401,17 +401,33 @@ __global__ void __launch_bounds__(256) qk_weight_kernel(const float* partial, in
   }
 }
 
-// Tokens of a tile: about 256 rows, at most kMaxTokens tables of turns.
-int tile_tokens(const QkProblem& p) {
-  const int heads = p.Hq > p.Hk ? p.Hq : p.Hk, t = 256 / heads;
-  return t < 1 ? 1 : t > kMaxTokens ? kMaxTokens : t;
+// Tokens of a tile: about 256 rows, at most kMaxTokens tables of turns, and then
+// as many fewer as spread the tiles evenly over `ctas` that run at once (B4 T4096
+// H16 D128: 16 tokens are 1.73 waves of the forward, 60.4 us, 14 are 1.98, 56.6;
+// in the gradient 16 are 4.6 rounds, 91.8 us, 15 are 4.9, 89.9; one token of 64
+// sequences H32 takes 2.7 us in 64 tiles, 7.2 in 8).
+int tile_tokens(const QkProblem& p, long long ctas) {
+  const int heads = p.Hq > p.Hk ? p.Hq : p.Hk;
+  int t = 256 / heads;
+  t = t < 1 ? 1 : t > kMaxTokens ? kMaxTokens : t;
+  const long long N = (long long)p.B * p.T, waves = ((N + t - 1) / t + ctas - 1) / ctas;
+  return (int)((N + waves * ctas - 1) / (waves * ctas));
 }
 
-// With tiles enough for four CTAs on every SM, one CTA takes queries and keys, so
-// that a token's sines are formed once; with fewer the two run side by side.  One
-// CTA | two, H16 D128: 16384 tokens 56.2 | 57.6 us, 9472 (592 tiles) 31.9 | 33.6,
-// 4096 19.4 | 15.3, 1024 13.0 | 7.8; a token of 64 sequences H32 12.3 | 7.2.
-constexpr unsigned kManyTiles = 148 * 4;
+// CTAs of the forward that run at once (four to an SM) and of the gradient, for
+// each tensor: the silu's derivative takes registers for two CTAs an SM instead
+// of three.
+constexpr int kFwdCtas = 148 * 4;
+int bwd_ctas(bool silu) { return silu ? 148 : 148 * 3 / 2; }
+
+// With tokens enough for one tile of 256 rows on every place, one CTA takes queries
+// and keys, so that a token's sines are formed once; with fewer the two run side
+// by side.  One CTA | two, H16 D128 in tiles of 16 tokens: 16384 tokens 56.2 | 57.6
+// us, 9472 31.9 | 33.6, 4096 19.4 | 15.3, 1024 13.0 | 7.8.
+bool one_cta(const QkProblem& p) {
+  const int heads = p.Hq > p.Hk ? p.Hq : p.Hk, t = 256 / heads;
+  return (long long)p.B * p.T >= (long long)kFwdCtas * (t < 1 ? 1 : t > kMaxTokens ? kMaxTokens : t);
+}
 
 // f(INTER, L2, SILU) for the problem's options.
 template <typename F>
@@ -436,9 +452,10 @@ void by_options(const QkProblem& p, F f) {
 
 template <typename TI, int D>
 cudaError_t fwd(const QkProblem& p, cudaStream_t st) {
-  const int tokens = tile_tokens(p);
+  const bool both_tensors = one_cta(p);
+  const int tokens = tile_tokens(p, both_tensors ? kFwdCtas : kFwdCtas / 2);
   const unsigned tiles = (unsigned)(((long long)p.B * p.T + tokens - 1) / tokens);
-  const dim3 grid(tiles, tiles >= kManyTiles ? 1 : 2);
+  const dim3 grid(tiles, both_tensors ? 1 : 2);
   const size_t smem = (size_t)tokens * p.rot * sizeof(float);
   by_options(p, [&](auto inter, auto l2, auto silu) {
     qk_fwd_kernel<TI, D, inter(), l2(), silu()><<<grid, kThreads, smem, st>>>(p, tokens);
@@ -448,7 +465,7 @@ cudaError_t fwd(const QkProblem& p, cudaStream_t st) {
 
 template <typename TI, typename TG, int D>
 cudaError_t bwd(const QkProblem& p, cudaStream_t st) {
-  const int tokens = tile_tokens(p);
+  const int tokens = tile_tokens(p, bwd_ctas(p.silu));
   const unsigned ctas = (unsigned)qk_bwd_ctas(p.B, p.T, p.Hq, p.Hk, p.silu);
   const size_t smem = (size_t)tokens * p.rot * sizeof(float);
   by_options(p, [&](auto inter, auto l2, auto silu) {
@@ -469,15 +486,14 @@ cudaError_t bwd_d(const QkProblem& p, cudaStream_t st) {
 
 int qk_bwd_ctas(int B, int T, int Hq, int Hk, int silu) {
   QkProblem p{};
+  p.B = B;
+  p.T = T;
   p.Hq = Hq;
   p.Hk = Hk;
-  const int tokens = tile_tokens(p);
-  const long long tiles = ((long long)B * T + tokens - 1) / tokens;
-  // times two tensors: one wave of what is resident on 148 SMs (92 us at B4 T4096
-  // H16 D128; a third more CTAs, and so a second wave, 113 us).  The silu's
-  // derivative takes registers for two CTAs an SM instead of three.
-  const long long ctas = silu ? 148 : 148 * 3 / 2;
-  return (int)(tiles < ctas ? tiles : ctas);
+  // one wave of what is resident (92 us at B4 T4096 H16 D128; a third more CTAs,
+  // and so a second wave, 113 us)
+  const long long tokens = tile_tokens(p, bwd_ctas(silu)), tiles = ((long long)B * T + tokens - 1) / tokens;
+  return (int)(tiles < bwd_ctas(silu) ? tiles : bwd_ctas(silu));
 }
 
 cudaError_t launch_qk_fwd(const QkProblem& p, cudaStream_t st) {
