@@ -29,34 +29,71 @@
 // chunks of each head (`out` without stored states): the same products without
 // the states' way through memory.
 //
-// Bound by the products' shared-memory operands and their multiply-adds (float32
-// has no tensor path); short sequences by the launches.  The gradient of a
-// ragged B2 H3 T777 Dk 128 Dv 64 takes 66 us, the forward of B1 H4 T100 D64 19 us.
+// Bound by the products' operands on their way out of shared memory (float32 has
+// no tensor path), short sequences by the launches.  Read along the depth four
+// at a time: the gradient of B2 H16 T1024 D128 434 us, of B2 H3 T777 Dk 128 Dv 64
+// 53, the forward of the first 210, of B1 H2 T256 D64 14.5; one at a time 791,
+// 64, 309 and 18.6.
 #include "kernels.h"
 
 namespace dn {
 namespace {
 
-constexpr int C = kGatedSimtChunk, kThreads = 256, NV = 32, CP = C + 1;
+constexpr int C = kGatedSimtChunk, kThreads = 256, NV = 32, CP = C + 4;
 static_assert(C == 32, "one lane per token of a chunk");
 
-// acc[x][y] += sum_{k < nk} A[(r0 + 16 x) ars + k acs] B[k brs + (c0 + 16 y) bcs]
-// for thread (r0, c0) of the CTA's 16 x 16 grid.
-template <int RX, int RY>
-__device__ __forceinline__ void product(int nk, const float* A, int ars, int acs, const float* B, int brs, int bcs,
+// acc[x][y] += sum_{k < nk} A(r0 + 16 x, k) B(k, c0 + 16 y) for thread (r0, c0) of
+// the CTA's 16 x 16 grid.  AK: A(i, k) = A[i * ap + k], else A[k * ap + i]; BK:
+// B(k, j) = B[j * bp + k], else B[k * bp + j].  What runs along k is read four at
+// a time: the operands' way out of shared memory is what the products wait for.
+// Pitches are 4 over a power of two, so that eight rows' pieces meet in no bank.
+template <int RX, int RY, bool AK, bool BK>
+__device__ __forceinline__ void product(int nk, const float* A, int ap, const float* B, int bp,
                                         float (&acc)[RX][RY]) {
   const int r0 = threadIdx.x >> 4, c0 = threadIdx.x & 15;
 #pragma unroll 4
-  for (int k = 0; k < nk; ++k) {
-    float a[RX], b[RY];
+  for (int k = 0; k < nk; k += 4) {
+    float a[RX][4], b[RY][4];
 #pragma unroll
-    for (int x = 0; x < RX; ++x) a[x] = A[(r0 + 16 * x) * ars + k * acs];
+    for (int x = 0; x < RX; ++x) {
+      const int i = r0 + 16 * x;
+      if (AK) {
+        const float4 v = *reinterpret_cast<const float4*>(A + i * ap + k);
+        a[x][0] = v.x; a[x][1] = v.y; a[x][2] = v.z; a[x][3] = v.w;
+      } else {
 #pragma unroll
-    for (int y = 0; y < RY; ++y) b[y] = B[k * brs + (c0 + 16 * y) * bcs];
+        for (int e = 0; e < 4; ++e) a[x][e] = A[(k + e) * ap + i];
+      }
+    }
 #pragma unroll
-    for (int x = 0; x < RX; ++x)
+    for (int y = 0; y < RY; ++y) {
+      const int j = c0 + 16 * y;
+      if (BK) {
+        const float4 v = *reinterpret_cast<const float4*>(B + j * bp + k);
+        b[y][0] = v.x; b[y][1] = v.y; b[y][2] = v.z; b[y][3] = v.w;
+      } else {
 #pragma unroll
-      for (int y = 0; y < RY; ++y) acc[x][y] = fmaf(a[x], b[y], acc[x][y]);
+        for (int e = 0; e < 4; ++e) b[y][e] = B[(k + e) * bp + j];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int x = 0; x < RX; ++x)
+#pragma unroll
+        for (int y = 0; y < RY; ++y) acc[x][y] = fmaf(a[x][e], b[y][e], acc[x][y]);
+  }
+}
+
+// A tile of R rows of W floats, `stride` apart in global memory, `pitch` in shared
+// memory; rows from n on are zero.
+template <int R, int W>
+__device__ __forceinline__ void load_tile(float* dst, int pitch, const float* src, size_t stride, int n) {
+#pragma unroll 8
+  for (int i = threadIdx.x; i < R * W / 4; i += kThreads) {
+    const int r = i / (W / 4), d = i % (W / 4) * 4;
+    const float4 x = r < n ? *reinterpret_cast<const float4*>(src + r * stride + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+    *reinterpret_cast<float4*>(dst + r * pitch + d) = x;
   }
 }
 
@@ -95,9 +132,9 @@ __device__ __forceinline__ float chunk_decays(const float* alpha, int n, float* 
 template <int DK, int DV>
 __global__ void __launch_bounds__(kThreads) gated_simt_local_kernel(const GatedProblem p, float* S, float* R,
                                                                     float* gammas) {
-  constexpr int KP = DK + 1, VP = DV + 1, RK = DK / 16, RV = DV / 16;
+  constexpr int KP = DK + 4, VP = DV + 4, RK = DK / 16, RV = DV / 16;
   __shared__ float into[C], out[C];
-  extern __shared__ float sm[];
+  extern __shared__ __align__(16) float sm[];
   float* Xs = sm;           // C x KP
   float* Zs = Xs + C * KP;  // C x VP
   const int tid = threadIdx.x, r0 = tid >> 4, c0 = tid & 15;
@@ -107,8 +144,8 @@ __global__ void __launch_bounds__(kThreads) gated_simt_local_kernel(const GatedP
   const bool rev = blockIdx.y;
   const float* x = static_cast<const float*>(rev ? p.q : p.k) + (bh * T + t0) * DK;
   const float* z = static_cast<const float*>(rev ? p.dO : p.v) + (bh * T + t0) * DV;
-  for (int i = tid; i < C * DK; i += kThreads) Xs[(i / DK) * KP + i % DK] = i / DK < n ? x[i] : 0.f;
-  for (int i = tid; i < C * DV; i += kThreads) Zs[(i / DV) * VP + i % DV] = i / DV < n ? z[i] : 0.f;
+  load_tile<C, DK>(Xs, KP, x, DK, n);
+  load_tile<C, DV>(Zs, VP, z, DV, n);
   if (tid < 32) {
     const float g = chunk_decays(p.alpha ? p.alpha + bh * T + t0 : nullptr, n, into, out, nullptr);
     if (tid == 0 && !rev) gammas[blockIdx.x] = g;
@@ -117,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) gated_simt_local_kernel(const GatedP
   for (int i = tid; i < C * DK; i += kThreads) Xs[(i / DK) * KP + i % DK] *= rev ? into[i / DK] : out[i / DK];
   __syncthreads();
   float a[RK][RV] = {};
-  product<RK, RV>(C, Xs, 1, KP, Zs, VP, 1, a);
+  product<RK, RV, false, false>(C, Xs, KP, Zs, VP, a);
   float* dst = (rev ? R : S) + (size_t)blockIdx.x * DK * DV;
 #pragma unroll
   for (int xx = 0; xx < RK; ++xx)
@@ -168,9 +205,9 @@ __global__ void __launch_bounds__(kThreads) gated_simt_between_kernel(const Gate
 // too, from the stored states.
 template <int DK, bool PAR>
 __global__ void __launch_bounds__(kThreads) gated_simt_out_kernel(const GatedProblem p, const float* states) {
-  constexpr int KP = DK + 1, VP = NV + 1, RK = DK / 16;
+  constexpr int KP = DK + 4, VP = NV + 4, RK = DK / 16;
   __shared__ float into[C], out[C], gam;
-  extern __shared__ float sm[];
+  extern __shared__ __align__(16) float sm[];
   float* Ks = sm;               // C x KP
   float* Vs = Ks + C * KP;      // C x VP
   float* Ss = Vs + C * VP;      // DK x VP
@@ -198,15 +235,9 @@ __global__ void __launch_bounds__(kThreads) gated_simt_out_kernel(const GatedPro
   for (int c = only; c < (PAR ? only + 1 : nch); ++c) {
     const int t0 = c * C, n = min(C, T - t0);
     __syncthreads();  // the products of the chunk before have read the tiles
-    for (int i = tid; i < C * DK; i += kThreads) {
-      const int r = i / DK, d = i % DK;
-      Ks[r * KP + d] = r < n ? k[(size_t)(t0 + r) * DK + d] : 0.f;
-      Qs[r * KP + d] = r < n ? q[(size_t)(t0 + r) * DK + d] : 0.f;
-    }
-    for (int i = tid; i < C * NV; i += kThreads) {
-      const int r = i / NV, d = i % NV;
-      Vs[r * VP + d] = r < n ? v[(size_t)(t0 + r) * Dv + d] : 0.f;
-    }
+    load_tile<C, DK>(Ks, KP, k + (size_t)t0 * DK, DK, n);
+    load_tile<C, DK>(Qs, KP, q + (size_t)t0 * DK, DK, n);
+    load_tile<C, NV>(Vs, VP, v + (size_t)t0 * Dv, Dv, n);
     if (tid < 32) {
       const float g = chunk_decays(alpha ? alpha + t0 : nullptr, n, into, out, Ds);
       if (tid == 0) gam = g;
@@ -217,7 +248,7 @@ __global__ void __launch_bounds__(kThreads) gated_simt_out_kernel(const GatedPro
       for (int y = 0; y < 2; ++y) Ss[(r0 + 16 * xx) * VP + c0 + 16 * y] = s[xx][y];
     __syncthreads();
     float a[2][2] = {};
-    product<2, 2>(DK, Qs, KP, 1, Ks, 1, KP, a);
+    product<2, 2, true, true>(DK, Qs, KP, Ks, KP, a);
 #pragma unroll
     for (int xx = 0; xx < 2; ++xx)
 #pragma unroll
@@ -226,13 +257,13 @@ __global__ void __launch_bounds__(kThreads) gated_simt_out_kernel(const GatedPro
         Ps[i * CP + j] = j <= i ? a[xx][y] * Ds[i * CP + j] : 0.f;
       }
     float qs[2][2] = {};
-    product<2, 2>(DK, Qs, KP, 1, Ss, VP, 1, qs);
+    product<2, 2, true, false>(DK, Qs, KP, Ss, VP, qs);
     __syncthreads();
 #pragma unroll
     for (int xx = 0; xx < 2; ++xx)
 #pragma unroll
       for (int y = 0; y < 2; ++y) qs[xx][y] *= into[r0 + 16 * xx];
-    product<2, 2>(C, Ps, CP, 1, Vs, VP, 1, qs);
+    product<2, 2, true, false>(C, Ps, CP, Vs, VP, qs);
 #pragma unroll
     for (int xx = 0; xx < 2; ++xx)
 #pragma unroll
@@ -246,7 +277,7 @@ __global__ void __launch_bounds__(kThreads) gated_simt_out_kernel(const GatedPro
     for (int xx = 0; xx < RK; ++xx)
 #pragma unroll
       for (int y = 0; y < 2; ++y) s[xx][y] *= gam;
-    product<RK, 2>(C, Ks, 1, KP, Vs, VP, 1, s);
+    product<RK, 2, false, false>(C, Ks, KP, Vs, VP, s);
   }
   if (!PAR && p.S_out) {
 #pragma unroll
@@ -263,9 +294,9 @@ __global__ void __launch_bounds__(kThreads) gated_simt_out_kernel(const GatedPro
 template <int DK, int DV>
 __global__ void __launch_bounds__(kThreads) gated_simt_grad_kernel(const GatedProblem p, const float* Sst,
                                                                    const float* Rst) {
-  constexpr int KP = DK + 1, VP = DV + 1, RK = DK / 16, RV = DV / 16;
+  constexpr int KP = DK + 4, VP = DV + 4, RK = DK / 16, RV = DV / 16;
   __shared__ float into[C], out[C], gam, row[C], col[C], rr[C], ee[C], through[kThreads / 32];
-  extern __shared__ float sm[];
+  extern __shared__ __align__(16) float sm[];
   float* Qs = sm;
   float* Ks = Qs + C * KP;
   float* Vs = Ks + C * KP;
@@ -283,17 +314,11 @@ __global__ void __launch_bounds__(kThreads) gated_simt_grad_kernel(const GatedPr
   const float* k = static_cast<const float*>(p.k) + kbase;
   const float* v = static_cast<const float*>(p.v) + vbase;
   const float* dO = static_cast<const float*>(p.dO) + vbase;
-  for (int i = tid; i < C * DK; i += kThreads) {
-    const int r = i / DK, d = i % DK;
-    Qs[r * KP + d] = r < n ? q[i] : 0.f;
-    Ks[r * KP + d] = r < n ? k[i] : 0.f;
-  }
-  for (int i = tid; i < C * DV; i += kThreads) {
-    const int r = i / DV, d = i % DV;
-    Vs[r * VP + d] = r < n ? v[i] : 0.f;
-    Os[r * VP + d] = r < n ? dO[i] : 0.f;
-  }
-  for (int i = tid; i < DK * DV; i += kThreads) Hs[(i / DV) * VP + i % DV] = Sst[sbase + i];
+  load_tile<C, DK>(Qs, KP, q, DK, n);
+  load_tile<C, DK>(Ks, KP, k, DK, n);
+  load_tile<C, DV>(Vs, VP, v, DV, n);
+  load_tile<C, DV>(Os, VP, dO, DV, n);
+  load_tile<DK, DV>(Hs, VP, Sst + sbase, DV, DK);
   if (tid < 32) {
     const float g = chunk_decays(p.alpha ? p.alpha + bh * T + t0 : nullptr, n, into, out, Ds);
     if (tid == 0) gam = g;
@@ -301,8 +326,8 @@ __global__ void __launch_bounds__(kThreads) gated_simt_grad_kernel(const GatedPr
   __syncthreads();
   {
     float a[2][2] = {}, b[2][2] = {};
-    product<2, 2>(DK, Qs, KP, 1, Ks, 1, KP, a);
-    product<2, 2>(DV, Os, VP, 1, Vs, 1, VP, b);
+    product<2, 2, true, true>(DK, Qs, KP, Ks, KP, a);
+    product<2, 2, true, true>(DV, Os, VP, Vs, VP, b);
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -333,7 +358,7 @@ __global__ void __launch_bounds__(kThreads) gated_simt_grad_kernel(const GatedPr
   };
   {
     float in[2][RK] = {};
-    product<2, RK>(DV, Os, VP, 1, Hs, 1, VP, in);
+    product<2, RK, true, true>(DV, Os, VP, Hs, VP, in);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int i = r0 + 16 * x;
@@ -346,7 +371,7 @@ __global__ void __launch_bounds__(kThreads) gated_simt_grad_kernel(const GatedPr
       dot = rowdot16(dot);
       if (c0 == 0) rr[i] = dot;
     }
-    product<2, RK>(C, Bs, CP, 1, Ks, KP, 1, in);
+    product<2, RK, true, false>(C, Bs, CP, Ks, KP, in);
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -357,10 +382,12 @@ __global__ void __launch_bounds__(kThreads) gated_simt_grad_kernel(const GatedPr
   __syncthreads();
   {
     float sr = 0.f;  // <S, R>, while R takes the place of S
-    for (int i = tid; i < DK * DV; i += kThreads) {
-      const float x = Rst[sbase + i];
-      float* h = Hs + (i / DV) * VP + i % DV;
-      sr = fmaf(*h, x, sr);
+#pragma unroll 8
+    for (int i = tid; i < DK * DV / 4; i += kThreads) {
+      const float4 x = reinterpret_cast<const float4*>(Rst + sbase)[i];
+      float4* h = reinterpret_cast<float4*>(Hs + i / (DV / 4) * VP + i % (DV / 4) * 4);
+      const float4 y = *h;
+      sr = fmaf(y.x, x.x, fmaf(y.y, x.y, fmaf(y.z, x.z, fmaf(y.w, x.w, sr))));
       *h = x;
     }
 #pragma unroll
@@ -370,7 +397,7 @@ __global__ void __launch_bounds__(kThreads) gated_simt_grad_kernel(const GatedPr
   __syncthreads();
   {
     float in[2][RK] = {};
-    product<2, RK>(DV, Vs, VP, 1, Hs, 1, VP, in);
+    product<2, RK, true, true>(DV, Vs, VP, Hs, VP, in);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int j = r0 + 16 * x;
@@ -383,7 +410,7 @@ __global__ void __launch_bounds__(kThreads) gated_simt_grad_kernel(const GatedPr
       dot = rowdot16(dot);
       if (c0 == 0) ee[j] = dot;
     }
-    product<2, RK>(C, Bs, 1, CP, Qs, KP, 1, in);
+    product<2, RK, false, false>(C, Bs, CP, Qs, KP, in);
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -393,12 +420,12 @@ __global__ void __launch_bounds__(kThreads) gated_simt_grad_kernel(const GatedPr
   }
   {
     float in[2][RV] = {};
-    product<2, RV>(DK, Ks, KP, 1, Hs, VP, 1, in);
+    product<2, RV, true, false>(DK, Ks, KP, Hs, VP, in);
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int y = 0; y < RV; ++y) in[x][y] *= out[r0 + 16 * x];
-    product<2, RV>(C, As, 1, CP, Os, VP, 1, in);
+    product<2, RV, false, false>(C, As, CP, Os, VP, in);
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -429,7 +456,7 @@ __global__ void __launch_bounds__(kThreads) gated_simt_grad_kernel(const GatedPr
 
 template <int DK, int DV>
 constexpr size_t grad_smem() {
-  return sizeof(float) * (2 * C * (DK + 1) + 2 * C * (DV + 1) + 3 * C * CP + DK * (DV + 1));
+  return sizeof(float) * (2 * C * (DK + 4) + 2 * C * (DV + 4) + 3 * C * CP + DK * (DV + 4));
 }
 
 int chunks(const GatedProblem& p) { return (p.T + C - 1) / C; }
@@ -442,7 +469,7 @@ cudaError_t prepare(K kern, size_t smem) {
 template <int DK, bool PAR>
 cudaError_t outputs(const GatedProblem& p, const float* states, cudaStream_t stream) {
   auto kern = gated_simt_out_kernel<DK, PAR>;
-  constexpr size_t smem = sizeof(float) * (2 * C * (DK + 1) + (C + DK) * (NV + 1) + 2 * C * CP);
+  constexpr size_t smem = sizeof(float) * (2 * C * (DK + 4) + (C + DK) * (NV + 4) + 2 * C * CP);
   cudaError_t e = prepare(kern, smem);
   if (e != cudaSuccess) return e;
   const size_t grid = (size_t)p.B * p.H * (p.Dv / NV) * (PAR ? chunks(p) : 1);
@@ -454,7 +481,7 @@ cudaError_t outputs(const GatedProblem& p, const float* states, cudaStream_t str
 template <int DK, int DV>
 cudaError_t states(const GatedProblem& p, float* S, float* R, float* gammas, cudaStream_t stream) {
   auto kern = gated_simt_local_kernel<DK, DV>;
-  constexpr size_t smem = sizeof(float) * C * (DK + DV + 2);
+  constexpr size_t smem = sizeof(float) * C * (DK + DV + 8);
   cudaError_t e = prepare(kern, smem);
   if (e != cudaSuccess) return e;
   const unsigned dirs = R ? 2 : 1;
@@ -486,12 +513,13 @@ size_t gamma_floats(size_t BH, int T) { return (BH * ((T + C - 1) / C) + 63) / 6
 }  // namespace
 
 // The forward walks the chunks of each head where one chunk is all there is, or
-// where 32-column slices of heads fill the GPU twice over.  Measured (D128, T512;
-// walk | chunks side by side): 64 heads, 256 slices 300 | 307 us, 72 heads 300 |
-// 343, 80 heads, a third wave of CTAs, 403 | 389, 128 heads 588 | 601; B2 H8 T128
-// D64 39 | 19.
+// where 32-column slices of heads fill the GPU four times over and the stored
+// states would only be memory.  Measured (T512; walk | chunks side by side, us):
+// D128 32 heads 135 | 111, 48 218 | 161, 64 229 | 211, 72 229 | 240, 80 (a third
+// wave of CTAs) 310 | 273, 128 444 | 428; D64 296 heads, 592 slices, 244 | 252;
+// H4 T100 25 | 14.5.
 bool gated_simt_walks(int BH, int T, int Dv, int sms) {
-  return T <= C || (long long)BH * (Dv / NV) >= 2LL * sms;
+  return T <= C || (long long)BH * (Dv / NV) >= 4LL * sms;
 }
 
 size_t gated_simt_bytes(int BH, int T, int Dk, int Dv, int directions) {

@@ -329,6 +329,17 @@ def test_many_heads(dn):
 
 
 @gpu
+@pytest.mark.parametrize("Dk,Dv", DIMS)
+def test_many_heads_float32(dn, Dk, Dv):
+    """Heads that fill the GPU several times: each walks its chunks, S_out on S0."""
+    x = case(8, 40, 77, Dk, Dv, torch.float32, "wipes", True, 10)
+    o, S = check_fwd(dn, x, torch.float32)
+    S0 = x["S0"].clone()
+    o2, S2 = dn.gated_linear_attn_fwd(*pick(x, FWD[:4]), S0, S_out=S0)
+    assert torch.equal(o, o2) and torch.equal(S, S2)
+
+
+@gpu
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("Dk,Dv", DIMS)
 @pytest.mark.parametrize("B,H,gated", [(1, 1, True), (3, 5, False), (16, 33, True)])
