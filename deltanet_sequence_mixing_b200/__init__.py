@@ -59,9 +59,17 @@ def _need(t, name, dtype=None, device=None):
     return t
 
 
+def _indexed(device) -> torch.device:
+    """The device with its index: "cuda" is the current one, not one of its own."""
+    device = torch.device("cuda" if device is None else device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return device
+
+
 def workspace_for(device, nbytes: int = 256) -> torch.Tensor:
     """A cleared device workspace of at least ``nbytes``, cached per device."""
-    device = torch.device(device)
+    device = _indexed(device)
     ws = _workspaces.get(device)
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
@@ -569,14 +577,13 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, positio
 def deltanet_get_device_status(device=None, workspace=None) -> int:
     """Synchronise and return the sticky device status of ``workspace`` (or of the
     cached workspaces of ``device``: the first that is not DN_OK)."""
-    device = torch.device(device if device is not None else "cuda")
+    device = _indexed(device)
     ws = workspace if workspace is not None else workspace_for(device)
     status = lib().deltanet_get_device_status(_ptr(ws), _stream(device))
     if workspace is None and status == 0 and _stream_workspaces:
-        index = torch.cuda.current_device() if device.index is None else device.index
-        torch.cuda.synchronize(index)  # their streams may be gone by now
+        torch.cuda.synchronize(device)  # their streams may be gone by now
         for (i, _), kept in list(_stream_workspaces.items()):
-            if i == index and status == 0:
+            if i == device.index and status == 0:
                 status = lib().deltanet_get_device_status(_ptr(kept), _stream(device))
     return status
 
@@ -589,7 +596,7 @@ def deltanet_selftest_wait_timeout(wait_ns: int, workspace, device=None) -> int:
 
 
 def reset_device_status(device=None, workspace=None) -> None:
-    device = torch.device(device if device is not None else "cuda")
+    device = _indexed(device)
     ws = workspace if workspace is not None else workspace_for(device)
     check("deltanet_workspace_init",
           lib().deltanet_workspace_init(_ptr(ws), ws.numel(), _stream(device)))
