@@ -596,7 +596,11 @@ def deltanet_selftest_wait_timeout(wait_ns: int, workspace, device=None) -> int:
 
 
 def reset_device_status(device=None, workspace=None) -> None:
+    """Clear the status of ``workspace`` (or all that the query of ``device`` reads)."""
     device = _indexed(device)
-    ws = workspace if workspace is not None else workspace_for(device)
-    check("deltanet_workspace_init",
-          lib().deltanet_workspace_init(_ptr(ws), ws.numel(), _stream(device)))
+    clear = [workspace if workspace is not None else workspace_for(device)]
+    if workspace is None and _stream_workspaces:
+        torch.cuda.synchronize(device)  # a call in flight on another stream comes before the reset
+        clear += [kept for (i, _), kept in list(_stream_workspaces.items()) if i == device.index]
+    for ws in clear:
+        check("deltanet_workspace_init", lib().deltanet_workspace_init(_ptr(ws), ws.numel(), _stream(device)))

@@ -53,3 +53,20 @@ def test_a_device_has_one_word_whatever_it_is_called(host):
     assert m.deltanet_get_device_status("cuda:0") == 0
     m.reset_device_status()
     assert m.deltanet_get_device_status("cuda:1") == 0
+
+
+def test_reset_clears_all_that_the_query_reads(host):
+    plain, kept = m.workspace_for("cuda:1"), m._own_workspace(torch.device("cuda", 1), 4096)
+    other = m._own_workspace(torch.device("cuda", 0), 4096)
+    for ws in (plain, kept):
+        give_up(ws)
+        assert m.deltanet_get_device_status() == m._lib.DN_ERR_DEVICE_TIMEOUT
+        m.reset_device_status()
+        assert m.deltanet_get_device_status() == 0
+    give_up(other)
+    m.reset_device_status("cuda:1")
+    assert m.deltanet_get_device_status("cuda:0") == m._lib.DN_ERR_DEVICE_TIMEOUT
+    mine = m._own_workspace(torch.device("cuda", 1), 4096)
+    give_up(mine)
+    m.reset_device_status(workspace=plain)  # a workspace's reset is its own
+    assert m.deltanet_get_device_status() == m._lib.DN_ERR_DEVICE_TIMEOUT
