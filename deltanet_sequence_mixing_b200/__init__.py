@@ -30,7 +30,8 @@ __all__ = [
     "gated_linear_attn_fwd", "gated_linear_attn_bwd", "gated_linear_attn_decode_step",
     "qk_norm_rope_fwd", "qk_norm_rope_bwd",
     "workspace_for", "host_workspace_for",
-    "deltanet_get_device_status", "deltanet_selftest_wait_timeout", "DeltaNetError",
+    "deltanet_get_device_status", "deltanet_selftest_wait_timeout", "deltanet_selftest_wait_polls",
+    "DeltaNetError",
 ]
 
 _DT = {torch.float32: _lib.DN_F32, torch.bfloat16: _lib.DN_BF16}
@@ -593,6 +594,13 @@ def deltanet_selftest_wait_timeout(wait_ns: int, workspace, device=None) -> int:
     device = torch.device(device if device is not None else workspace.device)
     return lib().deltanet_selftest_wait_timeout(_ptr(workspace), workspace.numel(), int(wait_ns),
                                                 _stream(device))
+
+
+def deltanet_selftest_wait_polls(polls: int, workspace, device=None) -> int:
+    """The bounded-wait self test of the gated recurrence's kernels, whose waits
+    count polls; returns the launch status."""
+    device = torch.device(device if device is not None else workspace.device)
+    return lib().deltanet_selftest_wait_polls(_ptr(workspace), workspace.numel(), int(polls), _stream(device))
 
 
 def reset_device_status(device=None, workspace=None) -> None:

@@ -61,6 +61,7 @@ SIGNATURES = {
     "qk_norm_rope_bwd": (_i, [_vp] * 12 + [_i] * 6 + [_ll] * 13 + [_f, _u, _i, _i, _vp, _sz, _vp]),
     "deltanet_get_device_status": (_i, [_vp, _vp]),
     "deltanet_selftest_wait_timeout": (_i, [_vp, _sz, _ll, _vp]),
+    "deltanet_selftest_wait_polls": (_i, [_vp, _sz, _i, _vp]),
     "deltanet_status_string": (ctypes.c_char_p, [_i]),
     "deltanet_version": (_i, []),
 }

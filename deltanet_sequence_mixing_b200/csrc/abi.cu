@@ -1023,6 +1023,13 @@ int deltanet_selftest_wait_timeout(void* workspace, size_t ws_bytes, long long w
                                            static_cast<cudaStream_t>(cuda_stream)));
 }
 
+int deltanet_selftest_wait_polls(void* workspace, size_t ws_bytes, int polls, void* cuda_stream) {
+  if (!workspace || ws_bytes < kStatusBytes) return DN_ERR_WORKSPACE;
+  if (polls < 1 || polls > 10000) return DN_ERR_INVALID_ARG;
+  return map_cuda(dn::launch_wait_polls_selftest(static_cast<unsigned int*>(workspace), polls,
+                                                 static_cast<cudaStream_t>(cuda_stream)));
+}
+
 const char* deltanet_status_string(int status) {
   switch (status) {
     case DN_OK: return "ok";

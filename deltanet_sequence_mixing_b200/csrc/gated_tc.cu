@@ -108,15 +108,18 @@ enum : uint32_t { C_FULL = 0, C_FREE = 16, C_VT = 32, C_DS = 48, C_DSFREE = 64, 
 // mbar_wait made short, its limit in polls instead of nanoseconds.  The roles of
 // a kernel run different code at the same time and wait at some thirty places;
 // where their loops together outgrow the SM's instruction cache, every warp
-// stalls on fetches.  A poll sleeps until the phase completes or the hint runs
-// out, so 2^15 of them are some seconds; polls that return at once are still a
-// millisecond, a hundred times the longest wait of a running pipeline.  Whoever
-// gives up says so and leaves; who waits for it runs out in turn.
+// stalls on fetches.  A poll sleeps until the phase completes or the hint of 200
+// us runs out, so 2^15 of them are up to 6.5 seconds.  Polls that come back at
+// once are still about a millisecond; the longest wait of a running pipeline is
+// that for a late segment's state, 0.25 us for each segment before it, 37 us for
+// the 148 that a head of 64 columns can be cut into on 148 SMs.  Whoever gives up
+// says so and leaves; who waits for it runs out in turn.
+constexpr int kWaitPolls = 32768;
 __device__ __noinline__ void give_up(unsigned int* status) {
   if (status) atomicOr(status, kStatusTimeoutBit);
 }
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, unsigned int* status) {
-  int polls = 32768;
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, unsigned int* status,
+                                         int polls = kWaitPolls) {
 #pragma unroll 1
   while (!mbar_try_wait_suspend(bar, parity)) {
     if (--polls == 0) {
@@ -1446,6 +1449,16 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   if (warp == kWarpMma) tmem_dealloc(tmem, 512);
 }
 
+// Nothing ever arrives on the barrier: the wait runs out after `polls` polls.
+__global__ void wait_polls_selftest_kernel(unsigned int* status, int polls) {
+  __shared__ __align__(8) uint64_t bar;
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&bar), 1);
+    fence_mbar_init();
+    (void)wait_bar(smem_u32(&bar), 0, status, polls);
+  }
+}
+
 template <int DK, bool GATED>
 cudaError_t launch_out(const GatedProblem& p, const GatedScan& s, cudaStream_t st) {
   CUtensorMap mq, mk, mv;
@@ -1601,6 +1614,11 @@ void gated_segments(int BH, int T, int Dv, int sms, int directions, int* G, int*
 
 size_t gated_segment_bytes(int BH, int G, int Dk, int Dv) {
   return G > 1 ? ((size_t)BH * G * 4 + 255) / 256 * 256 + (size_t)BH * G * Dk * Dv * 4 : 0;
+}
+
+cudaError_t launch_wait_polls_selftest(unsigned int* status, int polls, cudaStream_t st) {
+  wait_polls_selftest_kernel<<<1, 32, 0, st>>>(status, polls);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_gated_tc_fwd(const GatedProblem& p, cudaStream_t st) {

@@ -227,5 +227,7 @@ cudaError_t launch_qk_bwd(const QkProblem& p, cudaStream_t st);
 
 // Bounded-wait self test.
 cudaError_t launch_wait_selftest(unsigned int* status, long long wait_ns, cudaStream_t st);
+// The same of the gated recurrence's waits, which count polls.
+cudaError_t launch_wait_polls_selftest(unsigned int* status, int polls, cudaStream_t st);
 
 }  // namespace dn

@@ -436,6 +436,12 @@ int deltanet_selftest_wait_timeout(void *workspace, size_t ws_bytes, long long w
                                    void *cuda_stream);
 
 /*
+ * The same for the waits of the gated linear recurrence, whose limit is a
+ * number of polls (1 to 10,000 here, of at most 0.2 ms each).
+ */
+int deltanet_selftest_wait_polls(void *workspace, size_t ws_bytes, int polls, void *cuda_stream);
+
+/*
  * deltanet_chunk_fwd without a workspace argument, for callers that cannot
  * allocate device memory where they call the library: code running inside
  * another framework's allocator or memory-pool hooks (a cudaMalloc there would

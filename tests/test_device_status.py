@@ -70,3 +70,46 @@ def test_reset_clears_all_that_the_query_reads(host):
     give_up(mine)
     m.reset_device_status(workspace=plain)  # a workspace's reset is its own
     assert m.deltanet_get_device_status() == m._lib.DN_ERR_DEVICE_TIMEOUT
+
+
+def test_wait_selftest_refusals():
+    from deltanet_sequence_mixing_b200 import _lib as E
+    from deltanet_sequence_mixing_b200.build import build
+
+    build()
+    call = lambda ws=1 << 32, nb=256, polls=10: E.lib().deltanet_selftest_wait_polls(ws, nb, polls, None)
+    assert call(ws=None) == E.DN_ERR_WORKSPACE
+    assert call(nb=255) == E.DN_ERR_WORKSPACE
+    for polls in (0, -1, 10001):
+        assert call(polls=polls) == E.DN_ERR_INVALID_ARG
+
+
+# ----------------------------------------------------------------- on the GPU --
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dn():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    m.lib()
+    return m
+
+
+@gpu
+@pytest.mark.parametrize("polls", [1, 20])
+def test_a_counted_wait_runs_out(dn, polls):
+    """The recurrence's wait ends in a status that the host reads, and calls with
+    the same workspace work again after a reset."""
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    assert dn.deltanet_selftest_wait_polls(polls, ws) == 0
+    assert dn.deltanet_get_device_status(workspace=ws) == dn._lib.DN_ERR_DEVICE_TIMEOUT
+    dn.reset_device_status()
+    dn.reset_device_status(workspace=ws)
+    assert dn.deltanet_get_device_status(workspace=ws) == 0
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v = (torch.randn(1, 2, 200, 64, generator=g, device="cuda").bfloat16() for _ in range(3))
+    o, S = dn.gated_linear_attn_fwd(q, k, v, workspace=ws)
+    want = dn.gated_linear_attn_fwd(q, k, v)
+    assert torch.equal(o, want[0]) and torch.equal(S, want[1])
+    assert dn.deltanet_get_device_status(workspace=ws) == 0 and dn.deltanet_get_device_status() == 0
