@@ -251,7 +251,7 @@ def test_main_kernel(n, gated):
 
 @pytest.mark.parametrize("drop,place", [("done(B_PV, c - 2)", "scores"), ("done(B_DSFREE, c - 1)", "dS"),
                                         ("done(B_DS, c - 1)", "VT"), ("done(B_OFREE, c - 1)", "QS"),
-                                        ("done(B_OFREE, c - 3)", "decays")])
+                                        ("done(B_OFREE, 0)", "decays")])
 def test_the_model_sees_a_missing_wait(monkeypatch, drop, place):
     """The same programs with one of the waits left out of what was read."""
     waits, drop = _waits, _python(drop)
