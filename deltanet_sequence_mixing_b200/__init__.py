@@ -329,7 +329,8 @@ def _own_workspace(device, nbytes: int) -> torch.Tensor:
     device's cached status word (kernels only ever set bits in it).  Scratch is
     kept for each stream, whose calls follow one another; under graph capture,
     or where it is large, it comes from the caching allocator for this call
-    alone, so two graphs or two streams never share it."""
+    alone, so two graphs or two streams never share it.  Nobody reads the status
+    word in scratch: a timeout is in the device's own word, too."""
     capturing = torch.cuda.is_current_stream_capturing()
     if nbytes <= 256 and not capturing:
         return workspace_for(device)
@@ -338,7 +339,6 @@ def _own_workspace(device, nbytes: int) -> torch.Tensor:
     ws = _stream_workspaces.get((device.index, stream)) if keep else None
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        check("deltanet_workspace_init", lib().deltanet_workspace_init(_at(ws), nbytes, stream))
         if keep:
             _stream_workspaces[(device.index, stream)] = ws
     return ws
@@ -576,16 +576,17 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, positio
 
 
 def deltanet_get_device_status(device=None, workspace=None) -> int:
-    """Synchronise and return the sticky device status of ``workspace`` (or of the
-    cached workspaces of ``device``: the first that is not DN_OK)."""
+    """Synchronise and return the sticky device status of ``workspace``, or of
+    ``device``: of its cached workspace and, whatever workspace they had, of the
+    gated recurrence's calls on all of its streams."""
     device = _indexed(device)
-    ws = workspace if workspace is not None else workspace_for(device)
-    status = lib().deltanet_get_device_status(_ptr(ws), _stream(device))
-    if workspace is None and status == 0 and _stream_workspaces:
-        torch.cuda.synchronize(device)  # their streams may be gone by now
-        for (i, _), kept in list(_stream_workspaces.items()):
-            if i == device.index and status == 0:
-                status = lib().deltanet_get_device_status(_ptr(kept), _stream(device))
+    if workspace is not None:
+        return lib().deltanet_get_device_status(_ptr(workspace), _stream(device))
+    status = lib().deltanet_get_device_status(_ptr(workspace_for(device)), _stream(device))
+    if status == 0:
+        torch.cuda.synchronize(device)
+        with torch.cuda.device(device):
+            status = lib().deltanet_get_recurrence_status(_stream(device))
     return status
 
 
@@ -606,9 +607,9 @@ def deltanet_selftest_wait_polls(polls: int, workspace, device=None) -> int:
 def reset_device_status(device=None, workspace=None) -> None:
     """Clear the status of ``workspace`` (or all that the query of ``device`` reads)."""
     device = _indexed(device)
-    clear = [workspace if workspace is not None else workspace_for(device)]
-    if workspace is None and _stream_workspaces:
+    ws = workspace if workspace is not None else workspace_for(device)
+    check("deltanet_workspace_init", lib().deltanet_workspace_init(_ptr(ws), ws.numel(), _stream(device)))
+    if workspace is None:
         torch.cuda.synchronize(device)  # a call in flight on another stream comes before the reset
-        clear += [kept for (i, _), kept in list(_stream_workspaces.items()) if i == device.index]
-    for ws in clear:
-        check("deltanet_workspace_init", lib().deltanet_workspace_init(_ptr(ws), ws.numel(), _stream(device)))
+        with torch.cuda.device(device):
+            check("deltanet_clear_recurrence_status", lib().deltanet_clear_recurrence_status(_stream(device)))

@@ -59,6 +59,8 @@ SIGNATURES = {
     "qk_norm_rope_fwd": (_i, [_vp] * 8 + [_i] * 6 + [_ll] * 7 + [_f, _u, _i, _vp]),
     "qk_norm_rope_bwd_workspace_bytes": (_sz, [_i] * 5),
     "qk_norm_rope_bwd": (_i, [_vp] * 12 + [_i] * 6 + [_ll] * 13 + [_f, _u, _i, _i, _vp, _sz, _vp]),
+    "deltanet_get_recurrence_status": (_i, [_vp]),
+    "deltanet_clear_recurrence_status": (_i, [_vp]),
     "deltanet_get_device_status": (_i, [_vp, _vp]),
     "deltanet_selftest_wait_timeout": (_i, [_vp, _sz, _ll, _vp]),
     "deltanet_selftest_wait_polls": (_i, [_vp, _sz, _i, _vp]),

@@ -1015,6 +1015,19 @@ int deltanet_get_device_status(const void* workspace, void* cuda_stream) {
   return DN_ERR_CUDA;
 }
 
+int deltanet_get_recurrence_status(void* cuda_stream) {
+  void* word = nullptr;
+  if (dn::gated_device_word(&word) != cudaSuccess) return DN_ERR_CUDA;
+  return deltanet_get_device_status(word, cuda_stream);
+}
+
+int deltanet_clear_recurrence_status(void* cuda_stream) {
+  void* word = nullptr;
+  const cudaError_t e = dn::gated_device_word(&word);
+  if (e != cudaSuccess) return map_cuda(e);
+  return map_cuda(cudaMemsetAsync(word, 0, sizeof(unsigned int), static_cast<cudaStream_t>(cuda_stream)));
+}
+
 int deltanet_selftest_wait_timeout(void* workspace, size_t ws_bytes, long long wait_ns,
                                    void* cuda_stream) {
   if (!workspace || ws_bytes < kStatusBytes) return DN_ERR_WORKSPACE;

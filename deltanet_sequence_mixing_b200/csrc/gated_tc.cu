@@ -115,8 +115,12 @@ enum : uint32_t { C_FULL = 0, C_FREE = 16, C_VT = 32, C_DS = 48, C_DSFREE = 64, 
 // the 148 that a head of 64 columns can be cut into on 148 SMs.  Whoever gives up
 // says so and leaves; who waits for it runs out in turn.
 constexpr int kWaitPolls = 32768;
+// It says so in the workspace and, since a call's workspace may be gone before
+// anybody asks (scratch of one call, or of a graph), in a word of the device's own.
+__device__ unsigned int device_word;
 __device__ __noinline__ void give_up(unsigned int* status) {
   if (status) atomicOr(status, kStatusTimeoutBit);
+  atomicOr(&device_word, kStatusTimeoutBit);
 }
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, unsigned int* status,
                                          int polls = kWaitPolls) {
@@ -1622,6 +1626,8 @@ cudaError_t launch_wait_polls_selftest(unsigned int* status, int polls, cudaStre
   wait_polls_selftest_kernel<<<1, 32, 0, st>>>(status, polls);
   return cudaGetLastError();
 }
+
+cudaError_t gated_device_word(void** at) { return cudaGetSymbolAddress(at, device_word); }
 
 cudaError_t launch_gated_tc_fwd(const GatedProblem& p, cudaStream_t st) {
   if (p.alpha) return p.Dk == 128 ? fwd<128, true>(p, st) : fwd<64, true>(p, st);

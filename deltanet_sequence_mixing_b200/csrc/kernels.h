@@ -227,7 +227,9 @@ cudaError_t launch_qk_bwd(const QkProblem& p, cudaStream_t st);
 
 // Bounded-wait self test.
 cudaError_t launch_wait_selftest(unsigned int* status, long long wait_ns, cudaStream_t st);
-// The same of the gated recurrence's waits, which count polls.
+// The same of the gated recurrence's waits, which count polls.  They record a
+// timeout in a word of the current device, too.
+cudaError_t gated_device_word(void** at);
 cudaError_t launch_wait_polls_selftest(unsigned int* status, int polls, cudaStream_t st);
 
 }  // namespace dn

@@ -426,6 +426,16 @@ int qk_norm_rope_bwd(const void *q, const void *k, const void *dq_out, const voi
 int deltanet_get_device_status(const void *workspace, void *cuda_stream);
 
 /*
+ * The gated linear recurrence's calls record a timeout in a sticky word of the
+ * current device as well, whatever their workspace, which may be gone before
+ * the status is read: DN_ERR_DEVICE_TIMEOUT if any of them ran out of a wait
+ * since the word was last cleared.  The query synchronises `cuda_stream` alone;
+ * calls on other streams have to be waited for first.
+ */
+int deltanet_get_recurrence_status(void *cuda_stream);
+int deltanet_clear_recurrence_status(void *cuda_stream);
+
+/*
  * Self-test of the bounded-wait machinery: launches one CTA that waits on an
  * mbarrier nothing arrives on, for at most `wait_ns` nanoseconds (<= 2e9),
  * then records DN_ERR_DEVICE_TIMEOUT in the workspace status word and exits.

@@ -3,6 +3,7 @@
 On the CPU the library's calls are stood in for by ones that keep their words
 in host memory, so that a word can be set without a kernel.
 """
+import contextlib
 import ctypes
 
 import pytest
@@ -12,7 +13,10 @@ import deltanet_sequence_mixing_b200 as m
 
 
 class HostLib:
-    """The status calls on host memory."""
+    """The status calls on host memory; a device's own word by its index."""
+
+    def __init__(self):
+        self.current, self.words = 1, {0: 0, 1: 0}
 
     def deltanet_workspace_init(self, ws, nbytes, stream):
         ctypes.memset(ws, 0, 256)
@@ -22,11 +26,25 @@ class HostLib:
         at = ws.value if isinstance(ws, ctypes.c_void_p) else ws
         return -5 if ctypes.c_uint.from_address(at).value else 0
 
+    def deltanet_get_recurrence_status(self, stream):
+        return -5 if self.words[self.current] else 0
+
+    def deltanet_clear_recurrence_status(self, stream):
+        self.words[self.current] = 0
+        return 0
+
 
 @pytest.fixture
 def host(monkeypatch):
-    """The binding on host memory, device 1 of some current."""
+    """The binding on host memory, device 1 of two current."""
     lib, empty = HostLib(), torch.empty
+
+    @contextlib.contextmanager
+    def device(d):
+        before, lib.current = lib.current, d.index
+        yield
+        lib.current = before
+
     monkeypatch.setattr(m, "lib", lambda: lib)
     monkeypatch.setattr(m, "_workspaces", {})
     monkeypatch.setattr(m, "_stream_workspaces", {})
@@ -34,6 +52,7 @@ def host(monkeypatch):
     monkeypatch.setattr(m, "_current_raw_stream", lambda index: 7)
     monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: empty(*a, **k))
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "device", device)
     monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: None)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     return lib
@@ -56,20 +75,19 @@ def test_a_device_has_one_word_whatever_it_is_called(host):
 
 
 def test_reset_clears_all_that_the_query_reads(host):
-    plain, kept = m.workspace_for("cuda:1"), m._own_workspace(torch.device("cuda", 1), 4096)
-    other = m._own_workspace(torch.device("cuda", 0), 4096)
-    for ws in (plain, kept):
-        give_up(ws)
-        assert m.deltanet_get_device_status() == m._lib.DN_ERR_DEVICE_TIMEOUT
-        m.reset_device_status()
-        assert m.deltanet_get_device_status() == 0
-    give_up(other)
-    m.reset_device_status("cuda:1")
-    assert m.deltanet_get_device_status("cuda:0") == m._lib.DN_ERR_DEVICE_TIMEOUT
-    mine = m._own_workspace(torch.device("cuda", 1), 4096)
-    give_up(mine)
-    m.reset_device_status(workspace=plain)  # a workspace's reset is its own
+    plain = m.workspace_for("cuda:1")
+    give_up(plain)
     assert m.deltanet_get_device_status() == m._lib.DN_ERR_DEVICE_TIMEOUT
+    m.reset_device_status()
+    assert m.deltanet_get_device_status() == 0
+    host.words[0] = host.words[1] = 1
+    assert m.deltanet_get_device_status() == m._lib.DN_ERR_DEVICE_TIMEOUT
+    m.reset_device_status(workspace=plain)  # a workspace's reset is its own
+    assert m.deltanet_get_device_status(workspace=plain) == 0
+    assert m.deltanet_get_device_status() == m._lib.DN_ERR_DEVICE_TIMEOUT
+    m.reset_device_status("cuda:1")
+    assert m.deltanet_get_device_status() == 0
+    assert m.deltanet_get_device_status("cuda:0") == m._lib.DN_ERR_DEVICE_TIMEOUT
 
 
 def test_wait_selftest_refusals():
@@ -113,3 +131,51 @@ def test_a_counted_wait_runs_out(dn, polls):
     want = dn.gated_linear_attn_fwd(q, k, v)
     assert torch.equal(o, want[0]) and torch.equal(S, want[1])
     assert dn.deltanet_get_device_status(workspace=ws) == 0 and dn.deltanet_get_device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["no scratch", "kept", "replaced", "large", "captured"])
+def test_a_timeout_outlives_the_scratch(dn, kind):
+    """A wait that runs out in any workspace that a call can be given is reported
+    by the query without arguments, after the workspace is gone; a reset clears it."""
+    dev = torch.device("cuda", torch.cuda.current_device())
+    late = dn._lib.DN_ERR_DEVICE_TIMEOUT
+    dn.reset_device_status()
+    run = lambda nbytes: dn.deltanet_selftest_wait_polls(5, dn._own_workspace(dev, nbytes))
+    if kind == "captured":
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            assert run(4096) == 0
+        assert dn.deltanet_get_device_status() == 0
+        g.replay()
+    else:
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            assert run({"no scratch": 256, "large": dn._KEEP_BYTES + 256}.get(kind, 4096)) == 0
+            if kind == "replaced":
+                dn._own_workspace(dev, 1 << 20)
+        del s
+    assert dn.deltanet_get_device_status() == late
+    assert dn.deltanet_get_device_status() == late  # sticky
+    dn.reset_device_status()
+    assert dn.deltanet_get_device_status() == 0
+    if kind == "captured":
+        g.replay()
+        assert dn.deltanet_get_device_status() == late
+        dn.reset_device_status()
+
+
+@gpu
+def test_calls_leave_the_status_clear(dn):
+    """Scratch of every kind, eager and captured."""
+    dn.reset_device_status()
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    for B, H, T in ((1, 2, 100), (1, 1, 3000), (2, 20, 2000)):
+        q, k, v, dO = (torch.randn(B, H, T, 128, generator=gen, device="cuda").bfloat16() for _ in range(4))
+        call = lambda: (dn.gated_linear_attn_fwd(q, k, v), dn.gated_linear_attn_bwd(q, k, v, dO))
+        call()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        g.replay()
+    assert dn.deltanet_get_device_status() == 0
