@@ -69,13 +69,16 @@ def _indexed(device) -> torch.device:
 
 
 def workspace_for(device, nbytes: int = 256) -> torch.Tensor:
-    """A cleared device workspace of at least ``nbytes``, cached per device."""
+    """A cleared device workspace of at least ``nbytes``, cached per device; a
+    larger one in its place takes over the status."""
     device = _indexed(device)
     ws = _workspaces.get(device)
     if ws is None or ws.numel() < nbytes:
-        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+        before, ws = ws, torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
         check("deltanet_workspace_init",
               lib().deltanet_workspace_init(_ptr(ws), ws.numel(), _stream(device)))
+        if before is not None:
+            ws[:256].copy_(before[:256])
         _workspaces[device] = ws
     return ws
 

@@ -90,6 +90,14 @@ def test_reset_clears_all_that_the_query_reads(host):
     assert m.deltanet_get_device_status("cuda:0") == m._lib.DN_ERR_DEVICE_TIMEOUT
 
 
+def test_a_larger_workspace_keeps_the_status(host):
+    give_up(m.workspace_for("cuda:1"))
+    ws = m.workspace_for("cuda:1", 4096)
+    assert ws.numel() == 4096 and m.deltanet_get_device_status() == m._lib.DN_ERR_DEVICE_TIMEOUT
+    m.reset_device_status()
+    assert m.workspace_for("cuda:1", 8192).numel() == 8192 and m.deltanet_get_device_status() == 0
+
+
 def test_wait_selftest_refusals():
     from deltanet_sequence_mixing_b200 import _lib as E
     from deltanet_sequence_mixing_b200.build import build
