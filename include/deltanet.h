@@ -371,8 +371,9 @@ int gated_linear_attn_decode_step(const void *q, const void *k, const void *v,
  *
  *   q_weight, k_weight  (D) float32, or NULL for 1.
  *   positions   int64, element (b, t) at b * pos_stride_b + t (pos_stride_b = 0:
- *               one row for every b), or NULL for t.  Any value: the angle is
- *               formed in float64.
+ *               one row for every b), or NULL for t.  Any value: whole turns
+ *               are taken off in float64, past 2^24 in twice its precision
+ *               (for inv_freq up to 1 at most 2^-31 turns are left behind).
  *   inv_freq    (rot / 2) float32; unused (may be NULL) when rot == 0.
  *   q_out, k_out  (B,Hq,T,D), (B,Hk,T,D), element type dt.
  *   D 64 or 128; rot a multiple of 16, 0 <= rot <= D; Hq, Hk >= 0 (0: that
