@@ -30,7 +30,8 @@ constexpr int NC = 32, kThreads = 128, kLanes = NC / 4, kRows = kThreads / kLane
 template <typename TI, int DK>
 __global__ void __launch_bounds__(kThreads) gated_step_kernel(const GatedStepProblem p) {
   constexpr int RPT = DK / kRows;  // rows of a thread
-  __shared__ float qs[DK], ks[DK], red[kThreads / 32][NC];
+  __shared__ float qs[DK], ks[DK];
+  __shared__ __align__(16) float red[kThreads / 32][NC];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = tid % kLanes, r = tid / kLanes;
   const int nsl = p.Dv / NC;
   const size_t bh = blockIdx.x / nsl;

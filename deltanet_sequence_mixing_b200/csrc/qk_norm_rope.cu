@@ -231,7 +231,7 @@ struct Walk {
 template <typename TI, int D, bool INTER, bool L2, bool SILU>
 __global__ void __launch_bounds__(kThreads, 4) qk_fwd_kernel(const QkProblem p, int tokens) {
   constexpr int L = D / 16, ROWS = kThreads / L;
-  extern __shared__ float turns[];
+  extern __shared__ __align__(16) float turns[];
   __shared__ Tile tile[2];
   const int N = p.B * p.T, n0 = (int)blockIdx.x * tokens, nt = min(tokens, N - n0), half = p.rot / 2;
   const int l = threadIdx.x % L;
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_fwd_kernel(const QkProblem p, 
 template <typename TI, typename TG, int D, bool INTER, bool L2, bool SILU>
 __global__ void __launch_bounds__(kThreads, SILU ? 2 : 3) qk_bwd_kernel(const QkProblem p, int tokens) {
   constexpr int L = D / 16, ROWS = kThreads / L;
-  extern __shared__ float turns[];
+  extern __shared__ __align__(16) float turns[];
   __shared__ Tile tile, place;  // of x and of the derivative by the output; of the derivative by x
   __shared__ float part[kThreads / 32][D];
   const Side s = side_of(p, blockIdx.y);
