@@ -352,6 +352,8 @@ int validate_gated_sizes(int B, int H, int T, int Dk, int Dv, int dt) {
   if (dt != DN_F32 && dt != DN_BF16) return DN_ERR_UNSUPPORTED;
   if (B < 0 || H < 0 || T < 0) return DN_ERR_INVALID_ARG;
   if (!valid_dim(Dk) || !valid_dim(Dv)) return DN_ERR_UNSUPPORTED;
+  // tokens are numbered in an int, up to two chunks past T
+  if (T > INT_MAX - 2 * dn::kGatedChunk) return DN_ERR_UNSUPPORTED;
   // one CTA per (b, h, chunk, 32-column slice of Dv) at most, on a
   // one-dimensional grid
   const long long BH = (long long)B * H;
