@@ -323,6 +323,7 @@ def _need_shape(t, name, shape, dtype, device, optional=False):
 
 
 _stream_workspaces: dict = {}
+_scratch_devices: set = set()  # devices with calls that had scratch, on whatever stream
 _scratch_call = threading.Lock()  # a call's launches go together: threads may share a stream, and so its scratch
 _KEEP_BYTES = 32 << 20  # larger scratch is allocated for each call
 
@@ -342,6 +343,7 @@ def _own_workspace(device, nbytes: int) -> torch.Tensor:
     ws = _stream_workspaces.get((device.index, stream)) if keep else None
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        _scratch_devices.add(device.index)
         if keep:
             _stream_workspaces[(device.index, stream)] = ws
     return ws
@@ -587,7 +589,8 @@ def deltanet_get_device_status(device=None, workspace=None) -> int:
         return lib().deltanet_get_device_status(_ptr(workspace), _stream(device))
     status = lib().deltanet_get_device_status(_ptr(workspace_for(device)), _stream(device))
     if status == 0:
-        torch.cuda.synchronize(device)
+        if device.index in _scratch_devices:
+            torch.cuda.synchronize(device)  # their streams may be gone by now
         with torch.cuda.device(device):
             status = lib().deltanet_get_recurrence_status(_stream(device))
     return status
@@ -613,6 +616,7 @@ def reset_device_status(device=None, workspace=None) -> None:
     ws = workspace if workspace is not None else workspace_for(device)
     check("deltanet_workspace_init", lib().deltanet_workspace_init(_ptr(ws), ws.numel(), _stream(device)))
     if workspace is None:
-        torch.cuda.synchronize(device)  # a call in flight on another stream comes before the reset
+        if device.index in _scratch_devices:
+            torch.cuda.synchronize(device)  # a call in flight on another stream comes before the reset
         with torch.cuda.device(device):
             check("deltanet_clear_recurrence_status", lib().deltanet_clear_recurrence_status(_stream(device)))

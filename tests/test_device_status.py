@@ -48,6 +48,7 @@ def host(monkeypatch):
     monkeypatch.setattr(m, "lib", lambda: lib)
     monkeypatch.setattr(m, "_workspaces", {})
     monkeypatch.setattr(m, "_stream_workspaces", {})
+    monkeypatch.setattr(m, "_scratch_devices", set(), raising=False)
     monkeypatch.setattr(m, "_stream", lambda device: None)
     monkeypatch.setattr(m, "_current_raw_stream", lambda index: 7)
     monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: empty(*a, **k))
@@ -88,6 +89,20 @@ def test_reset_clears_all_that_the_query_reads(host):
     m.reset_device_status("cuda:1")
     assert m.deltanet_get_device_status() == 0
     assert m.deltanet_get_device_status("cuda:0") == m._lib.DN_ERR_DEVICE_TIMEOUT
+
+
+def test_the_query_waits_for_other_streams_only_where_they_have_scratch(host, monkeypatch):
+    """Waiting for the whole device would end another thread's graph capture."""
+    waited = []
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: waited.append(torch.device(device).index))
+    m._own_workspace(torch.device("cuda", 0), 4096)
+    m.deltanet_get_device_status("cuda:1")
+    m.reset_device_status("cuda:1")
+    assert waited == []
+    m._own_workspace(torch.device("cuda", 1), m._KEEP_BYTES + 1)
+    m.deltanet_get_device_status()
+    m.reset_device_status()
+    assert waited == [1, 1]
 
 
 def test_a_larger_workspace_keeps_the_status(host):
