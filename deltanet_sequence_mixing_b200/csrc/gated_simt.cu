@@ -29,8 +29,9 @@
 // chunks of each head (`out` without stored states): the same products without
 // the states' way through memory.
 //
-// Bound by the products' operands on their way out of shared memory (float32 has
-// no tensor path), short sequences by the launches.  Read along the depth four
+// Bound by the products' operands on their way out of shared memory, short
+// sequences by the launches.  (Tensor cores take float32 only as tf32, a product
+// as three of split operands; these kernels do not.)  Read along the depth four
 // at a time: the gradient of B2 H16 T1024 D128 434 us, of B2 H3 T777 Dk 128 Dv 64
 // 53, the forward of the first 210, of B1 H2 T256 D64 14.5; one at a time 791,
 // 64, 309 and 18.6.

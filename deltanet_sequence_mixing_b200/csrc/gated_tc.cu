@@ -914,8 +914,10 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 //   M = (Q K^T) * (dO V^T) * D,  r_i = q_i . G_i (dO S^T)_i,  e_j = k_j . c_j (V R^T)_j
 // (the first term: the suffix sum of row sums less column sums of M below its
 // diagonal, both from the same float32 values).  Its sums do not leave the
-// chunk, so no error travels along T; dO S^T and V R^T take hi and lo so that
-// r and e hold to float32, the outputs themselves to one rounding of A or B.
+// chunk, so no error travels along T; dO S^T and V R^T take hi and lo (16 bits)
+// so that r and e hold to float32, the outputs themselves to one rounding of A or
+// B.  Without a gate nothing needs more than the outputs, and S and R are read
+// rounded once (hi alone), as K R is in either case.
 //
 // One CTA per SM walks over the (b, h, chunk)s.  Everything of a chunk is in
 // shared memory at once except the states: R hi and S hi follow one another in a

@@ -178,7 +178,7 @@ size_t gated_bwd_bytes(int BH, int T, int G, int Dk, int Dv);
 cudaError_t launch_gated_tc_fwd(const GatedProblem& p, cudaStream_t st);
 cudaError_t launch_gated_tc_bwd(const GatedProblem& p, cudaStream_t st);
 // Whether the float32 forward walks the chunks of each head: one chunk, or heads
-// enough for two CTAs on every SM.  Otherwise (scratch of gated_simt_bytes,
+// enough for four CTAs (a head's 32 columns each) on every SM.  Otherwise (scratch of gated_simt_bytes,
 // directions 1) the chunks run side by side; the gradient always does
 // (directions 2).
 bool gated_simt_walks(int BH, int T, int Dv, int sms);

@@ -121,6 +121,8 @@ __device__ __forceinline__ void turn(V8& a, V8& b, const float* cs, const float*
   }
 }
 
+// The hardware's exponential, for float32 rows too: off by 2 + 1.2 |x| units in
+// the last place (4e-7 at 4, 2e-6 at -30, where silu is 3e-12).
 __device__ __forceinline__ float sigmoid_f(float x) { return 1.f / (1.f + __expf(-x)); }
 __device__ __forceinline__ float2 silu2(float2 x) { return make_float2(x.x * sigmoid_f(x.x), x.y * sigmoid_f(x.y)); }
 
@@ -435,8 +437,8 @@ int tile_tokens(const QkProblem& p, long long ctas) {
   return (int)((N + waves * ctas - 1) / (waves * ctas));
 }
 
-// CTAs of the forward that run at once (four to an SM) and of the gradient, for
-// each tensor: the silu's derivative takes registers for two CTAs an SM instead
+// CTAs of the forward that run at once (four to each of B200's 148 SMs; on fewer
+// the tiles only spread less evenly) and of the gradient, for each tensor: the silu's derivative takes registers for two CTAs an SM instead
 // of three.
 constexpr int kFwdCtas = 148 * 4;
 int bwd_ctas(bool silu) { return silu ? 148 : 148 * 3 / 2; }

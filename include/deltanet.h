@@ -303,8 +303,8 @@ int deltanet_chunk_bwd(const void *q, const void *k, const void *v,
  *
  *   q, k       (B,H,T,Dk), v (B,H,T,Dv), element type dt, 16-byte aligned.
  *   alpha      (B,H,T) float32 in [0,1], or NULL.  0 forgets everything before
- *              the token exactly (packed documents); a token with k = 0 and
- *              alpha = 1 leaves the state as it is (padding).
+ *              the token exactly (packed documents); a token with k = 0, a
+ *              finite v and alpha = 1 leaves the state as it is (padding).
  *   S0         (B,H,Dk,Dv) float32, or NULL for zero.
  *   o          (B,H,T,Dv), element type dt, 16-byte aligned.
  *   S_out      (B,H,Dk,Dv) float32, or NULL.  May equal S0.
@@ -312,7 +312,11 @@ int deltanet_chunk_bwd(const void *q, const void *k, const void *v,
  *              S_out, and the token buffers may then be NULL.
  *   workspace  gated_linear_attn_workspace_bytes(...) bytes, 16-byte aligned,
  *              cleared once with deltanet_workspace_init (the status word);
- *              calls that overlap on the GPU need one each.
+ *              calls that overlap on the GPU need one each.  bf16: the ends of
+ *              the segments, if any.  float32: 256 bytes where B H Dv / 32 is
+ *              at least four times the SMs or T <= 32; otherwise a state of
+ *              4 Dk Dv bytes for every 32 tokens of every (b, h), as much as q,
+ *              k, v and o together at Dk = Dv = 128.
  * The sizes depend on the current device's SM count, which must be that of the
  * call.  Arithmetic: bf16 inputs run on tensor cores with float32 accumulation
  * and state (products with rounded operands: the decayed scores and the state
@@ -335,8 +339,13 @@ int gated_linear_attn_fwd(const void *q, const void *k, const void *v,
  *     dlog_alpha (B,H,T) float32 = alpha * dL/dalpha (nullable; NULL when
  *                alpha is NULL);   dS0 (B,H,Dk,Dv) float32 (nullable).
  * dO has the shape and element type of o; dS_T is (B,H,Dk,Dv) float32 or NULL.
+ * bf16: the states between chunks of 128 tokens are kept as two bf16 values
+ * (16 bits; read as one without alpha, and where dv reads them), so dS0 and
+ * dlog_alpha hold to some 1e-5 of their norm; float32: in float32.
  * Outputs overlap neither inputs nor each other.  The workspace is
- * gated_linear_attn_bwd_workspace_bytes(...) bytes, otherwise as above.
+ * gated_linear_attn_bwd_workspace_bytes(...) bytes, otherwise as above: two
+ * states (S and its derivative) of 4 Dk Dv bytes for every 128 tokens (bf16) or
+ * 32 tokens (float32) of every (b, h), and the segments' ends.
  * T == 0 copies dS_T (or zeros) to dS0.  The result is deterministic.
  */
 size_t gated_linear_attn_bwd_workspace_bytes(int B, int H, int T, int Dk, int Dv, dn_dtype dt);
@@ -382,7 +391,8 @@ int gated_linear_attn_decode_step(const void *q, const void *k, const void *v,
  *               contiguous.  Bases and strides are multiples of 16 bytes
  *               (DN_ERR_ALIGNMENT otherwise); strides are not negative.
  *   eps         > 0 and finite.
- * Squares are summed in float32.  An output may not overlap an input or the
+ * Squares are summed in float32; the silu uses the hardware's exponential (off
+ * by 2 + 1.2 |x| units in float32's last place).  An output may not overlap an input or the
  * other output.
  */
 enum { DN_QK_L2 = 1, DN_QK_SILU = 2, DN_QK_INTERLEAVED = 4 };
