@@ -341,7 +341,8 @@ int gated_linear_attn_fwd(const void *q, const void *k, const void *v,
  * dO has the shape and element type of o; dS_T is (B,H,Dk,Dv) float32 or NULL.
  * bf16: the states between chunks of 128 tokens are kept as two bf16 values
  * (16 bits; read as one without alpha, and where dv reads them), so dS0 and
- * dlog_alpha hold to some 1e-5 of their norm; float32: in float32.
+ * dlog_alpha hold to some 1e-5 of the 2-norm of the terms that they are sums of;
+ * float32: in float32.
  * Outputs overlap neither inputs nor each other.  The workspace is
  * gated_linear_attn_bwd_workspace_bytes(...) bytes, otherwise as above: two
  * states (S and its derivative) of 4 Dk Dv bytes for every 128 tokens (bf16) or
